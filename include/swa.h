@@ -351,6 +351,130 @@ const char* swa_last_error(void);
 int swa_decode_noalloc(const void* q, const void* kring, const void* vring, const int64_t* pos,
                        void* out, int64_t B, int64_t H, int64_t D, int64_t W, void* stream);
 
+/* ---- A prefix shared by a batch, and a cache of a fixed budget ----
+ *
+ * The calls below take grouped heads: H query heads share Hkv key heads, H a multiple of Hkv
+ * (at most 1024 to one), query head h reading key head h / (H/Hkv).
+ *
+ * The budget cache of a stream has S slots a key head in no particular order. Slot s of (b,hk)
+ * holds a key row and a value row (kcache, vcache [B,Hkv,S,D] bf16), the position they belong
+ * to (pcache [B,Hkv,S] int64) and the attention weight that position has received so far
+ * (wcache [B,Hkv,S] fp32). A stream whose next token has position pos holds positions in
+ * slots 0 .. min(pos, S)-1; the other slots are never read. Below S tokens, position p is in
+ * slot p; from then on a new token takes the slot of the lightest token that is not among
+ * the newest `recent` (0 <= recent < S), the new one counted. Weights are compared as
+ * numbers: -0 equals 0, NaN counts as +infinity, ties go to the lowest slot (or position).
+ * Usual order: swa_forward_lse on the prompt, swa_key_weights, swa_cache_seed; then for each
+ * token swa_cache_append and swa_cache_decode.
+ */
+
+/*
+ * swa_key_weights: the attention weight that each key of a prompt received.
+ *
+ *   weights[b,hk,j] = sum over the query heads h of key head hk, sum over the counted queries
+ *                     i with 0 <= i - j < W, of exp(scale * q[b,h,i] . k[b,hk,j] - lse[b,h,i])
+ *
+ * with n = lens[b] (T when lens is NULL) tokens in stream b, of which the last `last` are
+ * counted as queries: max(0, n - last) <= i < n. Keys j >= n, and keys that no counted query
+ * sees, get 0. Rows of q, k and lse at or past n are not used.
+ *   q       : [B,H,T,D], k: [B,Hkv,T,D] of `dtype`; strides NULL (contiguous) or 6 element
+ *             strides q(b,h,t), k(b,h,t) as in swa_forward_ex.
+ *   lse     : [B,H,T] fp32 contiguous, as swa_forward_lse writes it for the same scale and W.
+ *   weights : [B,Hkv,T] fp32 contiguous, overwritten.
+ *   dtype   : SWA_BF16 (D 64 or 128, 16-byte aligned) or SWA_F32 (any D <= 4096).
+ *   scale   : finite, any sign.
+ * Scores, exponentials and sums are fp32. A lens[b] outside [0, T] is found on the device:
+ * that stream's weights are written as zeros and swa_device_status() reports
+ * SWA_ERR_INVALID_ARG. Errors: as swa_forward_ex, plus last < 1 or H not a multiple of Hkv ->
+ * SWA_ERR_INVALID_ARG.
+ */
+int swa_key_weights(const void* q, const void* k, const float* lse, const int64_t* lens, float* weights,
+                    int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t D, int64_t W, int64_t last,
+                    double scale, const int64_t* strides, int dtype, void* stream);
+
+/*
+ * swa_cache_seed: fill the budget cache from a prompt.
+ *
+ * Stream b has n = lens[b] tokens (T when lens is NULL). With n <= S all go to slots 0 .. n-1;
+ * otherwise the newest `recent` are kept and, of the older ones, the S - recent heaviest by
+ * `weights`. The kept positions fill slots 0 .. in ascending order, with their rows of k and v
+ * and their weights. Slots at or past min(n, S) are left as they were.
+ *   k, v    : [B,Hkv,T,D] bf16; strides NULL or 6 element strides k(b,h,t), v(b,h,t).
+ *   weights : [B,Hkv,T] fp32 contiguous (swa_key_weights).  D : 64 or 128.
+ * A lens[b] outside [0, T] leaves that stream's cache as it was and is reported by
+ * swa_device_status(). Errors: as swa_chunk_forward, plus recent outside [0, S) ->
+ * SWA_ERR_INVALID_ARG.
+ */
+int swa_cache_seed(const void* k, const void* v, const float* weights, const int64_t* lens, void* kcache,
+                   void* vcache, float* wcache, int64_t* pcache, int64_t B, int64_t Hkv, int64_t T, int64_t D,
+                   int64_t S, int64_t recent, const int64_t* strides, void* stream);
+
+/*
+ * swa_cache_append: one new token per stream into the budget cache.
+ *
+ * pos[b] is the position of stream b's new token, the number of tokens it had before. It goes
+ * to slot pos[b] while pos[b] < S. From then on it goes to the slot that holds pos[b] already,
+ * if there is one (a repeated call), else it evicts: among the slots whose position is at most
+ * pos[b] - recent, the one of least weight. The slot gets the token's rows, its position and
+ * weight 0.
+ *   k, v  : [B,Hkv,D] bf16 contiguous.   pos : [B] int64 on the device.
+ *   slots : [B,Hkv] int64, the slot taken (for a caller with state of its own per slot).
+ * A negative pos[b], or a head with no slot that may be evicted, leaves that head's cache as it
+ * was, writes slot -1 and is reported by swa_device_status() as SWA_ERR_INVALID_ARG.
+ * Errors: as swa_cache_seed.
+ */
+int swa_cache_append(const void* k, const void* v, void* kcache, void* vcache, float* wcache, int64_t* pcache,
+                     const int64_t* pos, int64_t* slots, int64_t B, int64_t Hkv, int64_t D, int64_t S,
+                     int64_t recent, void* stream);
+
+/*
+ * swa_cache_decode: one query per stream over the budget cache, and over a prefix that all
+ * streams share if there is one (P > 0).
+ *
+ * pos[b] is the position of stream b's query, whose key and value swa_cache_append has put into
+ * the cache. The query attends to the P prefix keys and to the cache's slots
+ * 0 .. min(pos[b]+1, S)-1, in one softmax, and each of these slots' weight grows by the sum of
+ * the probabilities that the query heads of its key head gave it. (Prefix keys are never
+ * evicted and have no weight.) Positions count from the end of the prefix.
+ *   q, out           : [B,H,D] bf16.
+ *   kprefix, vprefix : [Hkv,P,D] bf16; strides NULL (contiguous) or 4 element strides k(h,t),
+ *                      v(h,t). With P = 0 they and the strides are not read.
+ *   workspace        : caller-owned, workspace_bytes >= swa_cache_decode_workspace_bytes bytes,
+ *                      256-byte aligned; its contents need no preparation and mean nothing
+ *                      afterwards. Calls that may run at the same time need their own.
+ *   scale            : of the scores, > 0.      D : 64 or 128.
+ * Scores, statistics and sums are fp32. A negative pos[b] is found on the device: that stream's
+ * output is zeros, its weights stay and swa_device_status() reports SWA_ERR_INVALID_ARG.
+ * Errors: as swa_forward_ex, plus a workspace that is too short -> SWA_ERR_INVALID_ARG.
+ */
+int swa_cache_decode(const void* q, const void* kcache, const void* vcache, float* wcache, const int64_t* pos,
+                     const void* kprefix, const void* vprefix, void* out, void* workspace,
+                     int64_t workspace_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D,
+                     double scale, const int64_t* strides, void* stream);
+
+/* swa_cache_decode_workspace_bytes: bytes of workspace for these sizes, or -1 for invalid ones. */
+int64_t swa_cache_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D);
+
+/*
+ * swa_prefix_decode: one query per stream over a prefix that the whole batch shares and the
+ * stream's own W-slot ring, in one softmax.
+ *
+ * The prefix (a system prompt, the examples of a task) is stored once and always visible; the
+ * ring is swa_decode's, whose positions pos[b] count from the end of the prefix: the query sees
+ * the P prefix keys and ring slots 0 .. min(pos[b]+1, W)-1. The prefix is read once for all
+ * streams that share it.
+ *   q, out           : [B,H,D] bf16.    kring, vring : [B,Hkv,W,D] bf16.
+ *   kprefix, vprefix, strides, workspace, scale, D, negative positions: as swa_cache_decode
+ *                      (with swa_prefix_decode_workspace_bytes). P = 0 is the ring alone.
+ */
+int swa_prefix_decode(const void* q, const void* kprefix, const void* vprefix, const void* kring,
+                      const void* vring, const int64_t* pos, void* out, void* workspace, int64_t workspace_bytes,
+                      int64_t B, int64_t H, int64_t Hkv, int64_t W, int64_t P, int64_t D, double scale,
+                      const int64_t* strides, void* stream);
+
+/* swa_prefix_decode_workspace_bytes: bytes of workspace for these sizes, or -1 for invalid ones. */
+int64_t swa_prefix_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t W, int64_t P, int64_t D);
+
 /* ---- Host-side work planning (no GPU needed; the kernels use the same code) ---- */
 
 /*

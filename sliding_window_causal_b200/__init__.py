@@ -19,6 +19,19 @@ PyTorch only supplies device memory and streams.
     forward_lse(q, k, v, window)        (out, lse): the training forward
     backward(q, k, v, dout, window)     (dq, dk, dv) of the prefill (tensor cores for bf16)
     forward_host(...)                   prefill from pinned host tensors (copies included)
+
+Serving with grouped heads (H query heads over Hkv key heads), a prefix that the whole batch
+shares, and a cache of a fixed budget that forgets by attention weight instead of age:
+
+    prefix_decode(q, kprefix, vprefix, kring, vring, pos, window)
+                                        decode over a shared prefix and the stream's ring
+    key_weights(q, k, lse, window)      the attention weight each key of a prompt received
+    cache_seed(k, v, weights, kcache, vcache, wcache, pcache, recent)
+                                        a prompt's newest and heaviest keys into the cache
+    cache_append(k, v, kcache, vcache, wcache, pcache, pos, recent)
+                                        one token per stream, evicting the lightest
+    cache_decode(q, kcache, vcache, wcache, pos, kprefix=None, vprefix=None)
+                                        decode over the cache, whose weights it updates
 """
 import ctypes
 
@@ -29,7 +42,8 @@ __all__ = ["forward", "forward_lse", "backward", "band_weights", "decode", "chun
            "mha_workspace_bytes", "forward_host", "device_status", "tile_class", "valid_slots",
            "split_plan", "set_wait_limit_ns", "timeout_probe", "work_item", "backward_cta_tile",
            "set_prefill_mode", "prefill_auto_state", "PREFILL_AUTO", "PREFILL_ADAPTIVE", "PREFILL_FAST",
-           "SwaError"]
+           "prefix_decode", "key_weights", "cache_seed", "cache_append", "cache_decode",
+           "prefix_decode_workspace_bytes", "cache_decode_workspace_bytes", "SwaError"]
 
 
 def _torch():
@@ -326,6 +340,220 @@ def forward_host(q, k, v, window, out=None, device=None, staging=None, heads_per
                                              dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dout.data_ptr(),
                                              B, H, T, D, int(window), int(heads_per_group), _dtype_code(q),
                                              _stream_ptr(device)))
+    return out
+
+
+def _heads(H, Hkv):
+    if Hkv < 1 or H % Hkv:
+        raise ValueError(f"{H} query heads are not a multiple of {Hkv} key heads")
+
+
+def _positions(pos, B, name="pos"):
+    torch = _torch()
+    if pos.shape != (B,) or pos.dtype != torch.int64:
+        raise ValueError(f"{name} must be int64 [B]")
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, current stream of dev) with dev the current device."""
+    torch = _torch()
+    if dev.index == torch.cuda.current_device():
+        check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def key_weights(q, k, lse, window, lens=None, last=None, scale=None):
+    """The attention weight that each key of a prompt received: [B,Hkv,T] fp32, the sum over
+    the query heads of the key head and over the counted queries of the softmax weights.
+    q: [B,H,T,D], k: [B,Hkv,T,D] (bf16 with D in {64, 128}, or fp32 with any D <= 4096; any
+    (b,h,t) strides); lse: [B,H,T] fp32 as forward_lse returns it for the same window and
+    scale. lens: [B] int64 on the device, the tokens of each stream of a padded batch (None:
+    T each; keys past them get 0). last: count only each stream's last so many queries
+    (None: all)."""
+    torch = _torch()
+    if q.dim() != 4 or k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (q.shape[0], q.shape[2], q.shape[3]):
+        raise ValueError("q must be [B,H,T,D] and k [B,Hkv,T,D]")
+    if k.dtype != q.dtype:
+        raise TypeError("q and k must share one dtype")
+    B, H, T, D = q.shape
+    Hkv = k.shape[1]
+    _heads(H, Hkv)
+    if lse.shape != (B, H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [B,H,T]")
+    dev = _need_cuda(q, k, lse, contiguous=False)
+    if lens is not None:
+        _positions(lens, B, "lens")
+        _need_cuda(q, lens, contiguous=False)
+        lens = lens.contiguous()
+    out = torch.empty((B, Hkv, T), dtype=torch.float32, device=dev)
+    sc = 1.0 / D ** 0.5 if scale is None else float(scale)
+    _launch(dev, _native.lib().swa_key_weights, q.data_ptr(), k.data_ptr(), lse.data_ptr(),
+            None if lens is None else lens.data_ptr(), out.data_ptr(), B, H, Hkv, T, D, int(window),
+            max(T, 1) if last is None else int(last), sc, _bht_strides(q, k), _dtype_code(q))
+    return out
+
+
+def _budget_cache(kcache, vcache, wcache, pcache):
+    """(B, Hkv, S, D) of a budget cache; pcache may be None."""
+    torch = _torch()
+    if kcache.dim() != 4 or vcache.shape != kcache.shape:
+        raise ValueError("kcache and vcache must share one [B,Hkv,S,D] shape")
+    if kcache.dtype != torch.bfloat16 or vcache.dtype != torch.bfloat16:
+        raise TypeError("the cache's keys and values are bf16")
+    if wcache.shape != kcache.shape[:3] or wcache.dtype != torch.float32:
+        raise ValueError("wcache must be fp32 [B,Hkv,S]")
+    if pcache is not None and (pcache.shape != kcache.shape[:3] or pcache.dtype != torch.int64):
+        raise ValueError("pcache must be int64 [B,Hkv,S]")
+    return kcache.shape
+
+
+def cache_seed(k, v, weights, kcache, vcache, wcache, pcache, recent, lens=None):
+    """Fill a budget cache from a prompt, in place: of each stream's tokens (T, or lens[b])
+    the newest `recent` and the S - recent heaviest others by weights [B,Hkv,T] fp32
+    (key_weights), or all of them if they fit, in ascending order of position.
+    k, v: [B,Hkv,T,D] bf16, any (b,h,t) strides; kcache, vcache: [B,Hkv,S,D] bf16, wcache
+    [B,Hkv,S] fp32 (weights) and pcache [B,Hkv,S] int64 (positions), contiguous. Slots past
+    a stream's tokens are left as they were."""
+    torch = _torch()
+    B, Hkv, S, D = _budget_cache(kcache, vcache, wcache, pcache)
+    if k.dim() != 4 or v.shape != k.shape or (k.shape[0], k.shape[1], k.shape[3]) != (B, Hkv, D):
+        raise ValueError("k and v must share one [B,Hkv,T,D] shape that fits the cache")
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise TypeError("the cache's keys and values are bf16")
+    T = k.shape[2]
+    if weights.shape != (B, Hkv, T) or weights.dtype != torch.float32:
+        raise ValueError("weights must be fp32 [B,Hkv,T]")
+    dev = _need_cuda(kcache, vcache, wcache, pcache, weights)
+    _need_cuda(kcache, k, v, contiguous=False)
+    if lens is not None:
+        _positions(lens, B, "lens")
+        _need_cuda(kcache, lens)
+    _launch(dev, _native.lib().swa_cache_seed, k.data_ptr(), v.data_ptr(), weights.data_ptr(),
+            None if lens is None else lens.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), wcache.data_ptr(),
+            pcache.data_ptr(), B, Hkv, T, D, S, int(recent), _bht_strides(k, v))
+
+
+def cache_append(k, v, kcache, vcache, wcache, pcache, pos, recent):
+    """One new token per stream into a budget cache, in place: k, v [B,Hkv,D] bf16 at
+    position pos[b] (int64, the tokens the stream had before). It takes slot pos[b] while the
+    cache has room, else the slot that holds the position already, else that of the lightest
+    token among those at or before pos[b] - recent (lowest slot on ties); its weight starts
+    at 0. Returns the slots taken, [B,Hkv] int64."""
+    torch = _torch()
+    B, Hkv, S, D = _budget_cache(kcache, vcache, wcache, pcache)
+    if k.shape != (B, Hkv, D) or v.shape != k.shape:
+        raise ValueError("k and v must be [B,Hkv,D]")
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise TypeError("the cache's keys and values are bf16")
+    _positions(pos, B)
+    dev = _need_cuda(k, v, kcache, vcache, wcache, pcache, pos)
+    slots = torch.empty((B, Hkv), dtype=torch.int64, device=dev)
+    _launch(dev, _native.lib().swa_cache_append, k.data_ptr(), v.data_ptr(), kcache.data_ptr(), vcache.data_ptr(),
+            wcache.data_ptr(), pcache.data_ptr(), pos.data_ptr(), slots.data_ptr(), B, Hkv, D, S, int(recent))
+    return slots
+
+
+def _prefix(kprefix, vprefix, Hkv, D):
+    """(P, kprefix pointer, vprefix pointer, strides) of a shared prefix, or of none."""
+    torch = _torch()
+    if (kprefix is None) != (vprefix is None):
+        raise ValueError("give both kprefix and vprefix, or neither")
+    if kprefix is None:
+        return 0, None, None, None
+    if kprefix.dim() != 3 or vprefix.shape != kprefix.shape or (kprefix.shape[0], kprefix.shape[2]) != (Hkv, D):
+        raise ValueError("kprefix and vprefix must share one [Hkv,P,D] shape")
+    if kprefix.dtype != torch.bfloat16 or vprefix.dtype != torch.bfloat16:
+        raise TypeError("the prefix is bf16")
+    st = (*kprefix.stride()[:2], *vprefix.stride()[:2])
+    return kprefix.shape[1], kprefix.data_ptr(), vprefix.data_ptr(), (ctypes.c_int64 * 4)(*st)
+
+
+def _decode_out(q, out, workspace, need, dev):
+    torch = _torch()
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need_cuda(q, out)
+        if out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must match q")
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    else:
+        _need_cuda(q, workspace)
+    return out, workspace, workspace.numel() * workspace.element_size()
+
+
+def cache_decode_workspace_bytes(B, H, Hkv, S, P, D):
+    """Bytes of device workspace cache_decode needs."""
+    return int(_native.lib().swa_cache_decode_workspace_bytes(B, H, Hkv, S, P, D))
+
+
+def cache_decode(q, kcache, vcache, wcache, pos, kprefix=None, vprefix=None, out=None, scale=None, workspace=None):
+    """One query per stream over a budget cache, and over a prefix shared by all streams if
+    one is given, in one softmax; the cache's weights grow in place by the probabilities its
+    slots got. q: [B,H,D] bf16; kcache, vcache: [B,Hkv,S,D] bf16; wcache: [B,Hkv,S] fp32;
+    pos: [B] int64 on the device, the position of the query, whose key cache_append has
+    stored; kprefix, vprefix: [Hkv,P,D] bf16, any (h,t) strides. workspace: optional
+    preallocated CUDA tensor of at least cache_decode_workspace_bytes(...) bytes, not shared
+    by calls that may overlap. Returns out [B,H,D]."""
+    torch = _torch()
+    B, Hkv, S, D = _budget_cache(kcache, vcache, wcache, None)
+    if q.dim() != 3 or (q.shape[0], q.shape[2]) != (B, D):
+        raise ValueError("q must be [B,H,D] and the cache [B,Hkv,S,D]")
+    if q.dtype != torch.bfloat16:
+        raise TypeError("cache_decode takes bf16 q")
+    H = q.shape[1]
+    _heads(H, Hkv)
+    _positions(pos, B)
+    P, kp, vp, strides = _prefix(kprefix, vprefix, Hkv, D)
+    dev = _need_cuda(q, kcache, vcache, wcache, pos)
+    if P:
+        _need_cuda(q, kprefix, vprefix, contiguous=False)
+    lib = _native.lib()
+    need = lib.swa_cache_decode_workspace_bytes(B, H, Hkv, S, P, D)
+    out, workspace, have = _decode_out(q, out, workspace, need, dev)
+    sc = 1.0 / D ** 0.5 if scale is None else float(scale)
+    _launch(dev, lib.swa_cache_decode, q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), wcache.data_ptr(),
+            pos.data_ptr(), kp, vp, out.data_ptr(), workspace.data_ptr(), have, B, H, Hkv, S, P, D, sc, strides)
+    return out
+
+
+def prefix_decode_workspace_bytes(B, H, Hkv, W, P, D):
+    """Bytes of device workspace prefix_decode needs."""
+    return int(_native.lib().swa_prefix_decode_workspace_bytes(B, H, Hkv, W, P, D))
+
+
+def prefix_decode(q, kprefix, vprefix, kring, vring, pos, window, out=None, scale=None, workspace=None):
+    """One query per stream over a prefix that the whole batch shares and the stream's own
+    W-slot ring, in one softmax. q: [B,H,D] bf16; kprefix, vprefix: [Hkv,P,D] bf16, any (h,t)
+    strides, stored once and always visible (None: no prefix); kring, vring: [B,Hkv,W,D] bf16
+    as in decode; pos: [B] int64 on the device, the query's position counted from the end of
+    the prefix. workspace: optional preallocated CUDA tensor of at least
+    prefix_decode_workspace_bytes(...) bytes, not shared by calls that may overlap. Returns
+    out [B,H,D]."""
+    torch = _torch()
+    if q.dim() != 3 or kring.dim() != 4:
+        raise ValueError("q must be [B,H,D] and the rings [B,Hkv,W,D]")
+    B, H, D = q.shape
+    Hkv = kring.shape[1]
+    if kring.shape != (B, Hkv, window, D) or vring.shape != kring.shape:
+        raise ValueError("rings must be [B,Hkv,W,D] with W = window")
+    if q.dtype != torch.bfloat16 or kring.dtype != torch.bfloat16 or vring.dtype != torch.bfloat16:
+        raise TypeError("prefix_decode takes bf16 q and rings")
+    _heads(H, Hkv)
+    _positions(pos, B)
+    P, kp, vp, strides = _prefix(kprefix, vprefix, Hkv, D)
+    dev = _need_cuda(q, kring, vring, pos)
+    if P:
+        _need_cuda(q, kprefix, vprefix, contiguous=False)
+    lib = _native.lib()
+    need = lib.swa_prefix_decode_workspace_bytes(B, H, Hkv, window, P, D)
+    out, workspace, have = _decode_out(q, out, workspace, need, dev)
+    sc = 1.0 / D ** 0.5 if scale is None else float(scale)
+    _launch(dev, lib.swa_prefix_decode, q.data_ptr(), kp, vp, kring.data_ptr(), vring.data_ptr(), pos.data_ptr(),
+            out.data_ptr(), workspace.data_ptr(), have, B, H, Hkv, int(window), P, D, sc, strides)
     return out
 
 

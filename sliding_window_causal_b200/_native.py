@@ -13,7 +13,9 @@ LIB_PATH = os.path.join(_HERE, "_swa.so")
 EXPORTS = ("swa_forward", "swa_forward_ex", "swa_forward_host", "swa_band_weights", "swa_decode", "swa_decode_noalloc",
            "swa_chunk_forward", "swa_ring_append", "swa_mha_forward", "swa_mha_workspace_bytes",
            "swa_forward_lse", "swa_backward", "swa_backward_workspace_bytes", "swa_device_status", "swa_last_error", "swa_prefill_tile_class", "swa_prefill_work_item", "swa_backward_cta_tile", "swa_decode_valid_slots", "swa_decode_split_plan",
-           "swa_set_wait_limit_ns", "swa_timeout_probe", "swa_set_prefill_mode", "swa_prefill_auto_state")
+           "swa_set_wait_limit_ns", "swa_timeout_probe", "swa_set_prefill_mode", "swa_prefill_auto_state",
+           "swa_key_weights", "swa_cache_seed", "swa_cache_append", "swa_cache_decode",
+           "swa_cache_decode_workspace_bytes", "swa_prefix_decode", "swa_prefix_decode_workspace_bytes")
 
 SWA_F32, SWA_BF16 = 0, 1
 STATUS_NAMES = {0: "SWA_OK", 1: "SWA_ERR_INVALID_ARG", 2: "SWA_ERR_UNSUPPORTED",
@@ -91,6 +93,20 @@ def lib(path=None):
     h.swa_set_wait_limit_ns.restype = ctypes.c_uint64
     h.swa_timeout_probe.argtypes = [vp]
     h.swa_timeout_probe.restype = i32
+    h.swa_key_weights.argtypes = [vp] * 5 + [i64] * 7 + [ctypes.c_double, ctypes.POINTER(i64), i32, vp]
+    h.swa_key_weights.restype = i32
+    h.swa_cache_seed.argtypes = [vp] * 8 + [i64] * 6 + [ctypes.POINTER(i64), vp]
+    h.swa_cache_seed.restype = i32
+    h.swa_cache_append.argtypes = [vp] * 8 + [i64] * 5 + [vp]
+    h.swa_cache_append.restype = i32
+    h.swa_cache_decode.argtypes = [vp] * 9 + [i64] * 7 + [ctypes.c_double, ctypes.POINTER(i64), vp]
+    h.swa_cache_decode.restype = i32
+    h.swa_cache_decode_workspace_bytes.argtypes = [i64] * 6
+    h.swa_cache_decode_workspace_bytes.restype = i64
+    h.swa_prefix_decode.argtypes = [vp] * 8 + [i64] * 7 + [ctypes.c_double, ctypes.POINTER(i64), vp]
+    h.swa_prefix_decode.restype = i32
+    h.swa_prefix_decode_workspace_bytes.argtypes = [i64] * 6
+    h.swa_prefix_decode_workspace_bytes.restype = i64
     if path is None:
         _lib = h
     return h

@@ -11,7 +11,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "_swa.so")
-SOURCES = [os.path.join(CSRC, "swa_api.cu"), os.path.join(CSRC, "module.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("swa_api.cu", "module.cu", "cache_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "swa.h")]
 
 NVCC_FLAGS = [

@@ -16,4 +16,8 @@ int clear_error();
 int check_forward(const char* fn, const void* q, const void* k, const void* v, const void* out, int64_t B,
                   int64_t H, int64_t T, int64_t D, int64_t W, double scale, const int64_t* strides, int dtype,
                   int64_t st[4][3]);
+// The current device's status word (device address) and SM count.
+int device_info(int** status, int* num_sms);
+// The time limit of the kernels' bounded waits, in nanoseconds.
+uint64_t wait_limit_ns();
 }  // namespace swa_internal

@@ -1,0 +1,324 @@
+// attend.cuh: one query per stream over keys in memory (a prefix shared by all streams, the
+// stream's ring, the stream's budget cache), bf16, D = 64/128, G query heads to a key head.
+//
+// The softmax of a row is taken in splits of its keys, each an online softmax state
+//   m = max_j z_j,  l = sum_j 2^(z_j - m),  o = sum_j 2^(z_j - m) v_j,   z = scale log2(e) q.k,
+// and joined by finish_kernel: m* = max m, out = sum 2^(m - m*) o / sum 2^(m - m*) l.
+//
+// attend_kernel: CTA = (key head, 8 queries, split of the keys). The keys are read once for the
+// 8 queries that share them, so the kernel is bound by HBM: 4 D bytes a slot against 32 D
+// multiply-adds. The products go through m16n8k16 with the keys as the 16 rows (S^T = K Q^T
+// and O^T = V^T P^T), which spends no tile rows on missing queries. Every fragment comes
+// straight from 16-byte loads: the order of the head dimension inside a product is free as
+// long as K and Q agree (a lane's 16 bytes are two k-steps), and in O^T it is the order of
+// the output rows. P crosses from accumulator to operand layout by an 8x8 transpose inside
+// the warp. P is carried as two bf16 parts (hi + lo, 16 bits of weight), so that the output
+// is rounded once: the products are far from bounding the kernel. m, l, o are fp32; o and l
+// are rescaled only when a score passes m by more than 2^8.
+#pragma once
+#include <cuda_bf16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "decode.cuh"
+#include "ptx.cuh"
+
+namespace swa {
+
+constexpr int kAttendWarps = 4;
+constexpr int kAttendStep = 16 * kAttendWarps;  // slots a CTA takes per step
+constexpr int kAttendQueries = 8;               // queries a CTA serves
+constexpr float kAttendRescale = 8.f;
+
+// Where a call's queries, keys and partial states are. Row = b * H + h.
+struct AttendArgs {
+    const __nv_bfloat16* q;    // [B, H, D]
+    const __nv_bfloat16* k;    // ring or cache [B, Hkv, S, D]; prefix: (h, t) strides
+    const __nv_bfloat16* v;
+    const int64_t* pos;        // [B]; not read for the prefix
+    float2* ml;                // [B*H][NS] (m, l)
+    float* o;                  // [B*H][NS][D]
+    float* scores;             // [B*Hkv][G][S] z of every slot, or null
+    int64_t k_head, k_row, v_head, v_row;  // element strides
+    int B, H, Hkv, G, S;       // S: slots, or the prefix length
+    int chunk, split0, NS;     // keys a split takes, first split index, splits in all
+    float scale_log2;
+    int* status;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t word(const uint4& u, int w) { return w == 0 ? u.x : w == 1 ? u.y : w == 2 ? u.z : u.w; }
+
+// PREFIX: the keys are the shared prefix and the queries are all streams' (row r of key head hk
+// is stream r / G, head hk G + r % G); else the keys are stream b's slots 0 .. min(pos+1, S)-1.
+template <int D, bool PREFIX, bool SCORES>
+__global__ void __launch_bounds__(kAttendWarps * 32) attend_kernel(const AttendArgs a) {
+    constexpr int KL = D / 32;  // 16-byte pieces of a key row per lane
+    constexpr int VL = D / 64;  // 16-byte pieces of a value row per lane
+    constexpr int MT = D / 16;  // 16-row tiles of O^T
+    __shared__ float sm_m[kAttendWarps][kAttendQueries], sm_l[kAttendWarps][kAttendQueries];
+    __shared__ float sm_o[kAttendWarps][kAttendQueries][D + 8];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int s = blockIdx.y;
+    const int n_rows = PREFIX ? a.B * a.G : a.G;  // queries that share these keys
+    const int qtiles = (n_rows + kAttendQueries - 1) / kAttendQueries;
+    const int64_t unit = blockIdx.x / qtiles;  // hk, or b * Hkv + hk
+    const int q0 = (int)(blockIdx.x % qtiles) * kAttendQueries;
+    const int nq = min(kAttendQueries, n_rows - q0);
+    const int hk = PREFIX ? (int)unit : (int)(unit % a.Hkv);
+    const int64_t b0 = PREFIX ? 0 : unit / a.Hkv;
+    auto row_of = [&](int i) -> int64_t {  // query i of this CTA
+        const int r = q0 + i;
+        return PREFIX ? (int64_t)(r / a.G) * a.H + hk * a.G + r % a.G : b0 * a.H + hk * a.G + r;
+    };
+
+    int n = a.S;
+    if (!PREFIX) {
+        const int64_t P = a.pos[b0];
+        if (P < 0) {
+            if (tid == 0 && s == 0) atomicCAS(a.status, 0, kStatusInvalid);
+            n = 0;
+        } else {
+            n = (int)(P + 1 < (int64_t)a.S ? P + 1 : (int64_t)a.S);
+        }
+    }
+    const int r0 = s * a.chunk;
+    const int r1 = min(r0 + a.chunk, n);
+    if (r0 >= r1) {  // nothing of this split is valid
+        if (tid < nq) a.ml[row_of(tid) * a.NS + a.split0 + s] = make_float2(-INFINITY, 0.f);
+        return;
+    }
+
+    uint32_t qf[KL][4];  // B fragments of Q^T: query g
+    if (g < nq) {
+        const __nv_bfloat16* qr = a.q + row_of(g) * D;
+#pragma unroll
+        for (int i = 0; i < KL; ++i) {
+            const uint4 u = *reinterpret_cast<const uint4*>(qr + 32 * i + 8 * t);
+            qf[i][0] = u.x; qf[i][1] = u.y; qf[i][2] = u.z; qf[i][3] = u.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < KL; ++i) qf[i][0] = qf[i][1] = qf[i][2] = qf[i][3] = 0u;
+    }
+    const __nv_bfloat16* kb = a.k + unit * a.k_head + 8 * t;
+    const __nv_bfloat16* vb = a.v + unit * a.v_head + 8 * g;
+    float* zrow = SCORES ? a.scores + (unit * a.G + q0) * a.S : nullptr;
+
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // queries 2t, 2t+1
+    float o[MT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int base = r0 + 16 * warp; base < r1; base += kAttendStep) {
+        uint4 kr[2][KL], vr[4][VL];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int slot = base + g + 8 * x;
+#pragma unroll
+            for (int i = 0; i < KL; ++i) kr[x][i] = slot < r1 ? ld_stream_16(kb + slot * a.k_row + 32 * i) : zero;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int slot = base + 2 * t + (x & 1) + 8 * (x >> 1);
+#pragma unroll
+            for (int i = 0; i < VL; ++i) vr[x][i] = slot < r1 ? ld_stream_16(vb + slot * a.v_row + 64 * i) : zero;
+        }
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < KL; ++i) {
+            mma_bf16(c, kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y, qf[i][0], qf[i][1]);
+            mma_bf16(c, kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, qf[i][2], qf[i][3]);
+        }
+        const bool v0 = base + g < r1, v1 = base + g + 8 < r1;
+        const float z0 = v0 ? c[0] * a.scale_log2 : -INFINITY, z1 = v0 ? c[1] * a.scale_log2 : -INFINITY;
+        const float z2 = v1 ? c[2] * a.scale_log2 : -INFINITY, z3 = v1 ? c[3] * a.scale_log2 : -INFINITY;
+        if (SCORES) {
+            if (2 * t < nq) {
+                if (v0) zrow[(int64_t)(2 * t) * a.S + base + g] = z0;
+                if (v1) zrow[(int64_t)(2 * t) * a.S + base + g + 8] = z2;
+            }
+            if (2 * t + 1 < nq) {
+                if (v0) zrow[(int64_t)(2 * t + 1) * a.S + base + g] = z1;
+                if (v1) zrow[(int64_t)(2 * t + 1) * a.S + base + g + 8] = z3;
+            }
+        }
+        float t0 = fmaxf(z0, z2), t1 = fmaxf(z1, z3);
+        if (__any_sync(0xffffffffu, t0 > m0 + kAttendRescale || t1 > m1 + kAttendRescale)) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
+                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
+            }
+            const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+            const float f0 = m0 == -INFINITY ? 0.f : ptx::ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - n1);
+            m0 = n0;
+            m1 = n1;
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                o[i][0] *= f0;
+                o[i][1] *= f1;
+                o[i][2] *= f0;
+                o[i][3] *= f1;
+            }
+        }
+        const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+        const float p0 = ptx::ex2(z0 - u0), p1 = ptx::ex2(z1 - u1), p2 = ptx::ex2(z2 - u0), p3 = ptx::ex2(z3 - u1);
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        const uint32_t h01 = ptx::pack_bf16x2(p0, p1), h23 = ptx::pack_bf16x2(p2, p3);
+        const uint32_t e01 = ptx::pack_bf16x2(p0 - ptx::bf16lo_f32(h01), p1 - ptx::bf16hi_f32(h01));
+        const uint32_t e23 = ptx::pack_bf16x2(p2 - ptx::bf16lo_f32(h23), p3 - ptx::bf16hi_f32(h23));
+        const uint32_t bh0 = transpose_8x8(h01), bh1 = transpose_8x8(h23);
+        const uint32_t bl0 = transpose_8x8(e01), bl1 = transpose_8x8(e23);
+#pragma unroll
+        for (int i = 0; i < VL; ++i)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t x0 = word(vr[0][i], w), x1 = word(vr[1][i], w), x2 = word(vr[2][i], w), x3 = word(vr[3][i], w);
+                const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
+                const uint32_t a2 = __byte_perm(x2, x3, 0x5410), a3 = __byte_perm(x2, x3, 0x7632);
+                mma_bf16(o[4 * i + w], a0, a1, a2, a3, bh0, bh1);
+                mma_bf16(o[4 * i + w], a0, a1, a2, a3, bl0, bl1);
+            }
+    }
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+    }
+    if (g == 0) {
+        sm_m[warp][2 * t] = m0;
+        sm_m[warp][2 * t + 1] = m1;
+        sm_l[warp][2 * t] = l0;
+        sm_l[warp][2 * t + 1] = l1;
+    }
+#pragma unroll
+    for (int i = 0; i < VL; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int d = 64 * i + 8 * g + 2 * w;
+            *reinterpret_cast<float2*>(&sm_o[warp][2 * t][d]) = make_float2(o[4 * i + w][0], o[4 * i + w][2]);
+            *reinterpret_cast<float2*>(&sm_o[warp][2 * t + 1][d]) = make_float2(o[4 * i + w][1], o[4 * i + w][3]);
+        }
+    __syncthreads();
+    for (int x = tid; x < nq * (D / 4); x += kAttendWarps * 32) {
+        const int i = x / (D / 4), d = (x % (D / 4)) * 4;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kAttendWarps; ++w) M = fmaxf(M, sm_m[w][i]);
+        float L = 0.f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kAttendWarps; ++w) {
+            // a warp without a slot has l = 0 and o = 0
+            const float f = sm_m[w][i] == -INFINITY ? 0.f : ptx::ex2(sm_m[w][i] - M);
+            L = fmaf(sm_l[w][i], f, L);
+            const float4 v = *reinterpret_cast<const float4*>(&sm_o[w][i][d]);
+            A.x = fmaf(v.x, f, A.x);
+            A.y = fmaf(v.y, f, A.y);
+            A.z = fmaf(v.z, f, A.z);
+            A.w = fmaf(v.w, f, A.w);
+        }
+        const int64_t at = row_of(i) * a.NS + a.split0 + s;
+        *reinterpret_cast<float4*>(a.o + at * D + d) = A;
+        if (d == 0) a.ml[at] = make_float2(M, L);
+    }
+}
+
+// ------------------------------------------------------------------ joining the splits
+constexpr int kFinishThreads = 128;
+constexpr int kFinishSlots = 1024;  // slots of one key head that a CTA adds weights to
+
+// (m*, l*) of one row over its NS splits, by a whole warp.
+__device__ __forceinline__ float2 finish_ml(const float2* ml, int NS, int lane) {
+    float M = -INFINITY;
+    for (int s = lane; s < NS; s += 32) M = fmaxf(M, __ldcg(ml + s).x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    float L = 0.f;
+    for (int s = lane; s < NS; s += 32) {
+        const float2 e = __ldcg(ml + s);
+        if (e.x != -INFINITY) L = fmaf(e.y, ptx::ex2(e.x - M), L);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+    return make_float2(M, L);
+}
+
+// The first B*H CTAs each write one output row; the others add the attention weights of
+// kFinishSlots slots of one key head, w[slot] += sum over its G rows of 2^(z - m*) / l*, in
+// the fixed order of the heads.
+template <int D>
+__global__ void __launch_bounds__(kFinishThreads)
+    finish_kernel(const AttendArgs a, __nv_bfloat16* __restrict__ out, float* __restrict__ weights, int slot_blocks) {
+    __shared__ float sm[4][D];
+    extern __shared__ float sm_lse[];  // [G]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t rows = (int64_t)a.B * a.H;
+    ptx::grid_dependency_wait();
+    if (blockIdx.x < rows) {
+        const int64_t row = blockIdx.x;
+        __nv_bfloat16* orow = out + row * D;
+        if (a.pos[row / a.H] < 0) {
+            for (int d = tid; d < D; d += kFinishThreads) orow[d] = __float2bfloat16_rn(0.f);
+            return;
+        }
+        const float2* ml = a.ml + row * a.NS;
+        const float2 all = finish_ml(ml, a.NS, lane);
+        constexpr int E = D / 32;
+        float acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        for (int s = warp; s < a.NS; s += 4) {
+            const float m = __ldcg(ml + s).x;
+            if (m == -INFINITY) continue;
+            const float f = ptx::ex2(m - all.x);
+            const float* op = a.o + (row * a.NS + s) * D + lane;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(__ldcg(op + 32 * e), f, acc[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) sm[warp][lane + 32 * e] = acc[e];
+        __syncthreads();
+        if (tid < D) orow[tid] = __float2bfloat16_rn((sm[0][tid] + sm[1][tid] + sm[2][tid] + sm[3][tid]) / all.y);
+        return;
+    }
+    const int64_t x = blockIdx.x - rows;
+    const int64_t unit = x / slot_blocks;
+    const int s0 = (int)(x % slot_blocks) * kFinishSlots;
+    const int64_t b = unit / a.Hkv;
+    const int64_t P = a.pos[b];
+    const int n = P < 0 ? 0 : (int)(P + 1 < (int64_t)a.S ? P + 1 : (int64_t)a.S);
+    if (s0 >= n) return;
+    const int64_t row0 = b * a.H + (unit % a.Hkv) * a.G;
+    for (int h = warp; h < a.G; h += 4) {
+        const float2 all = finish_ml(a.ml + (row0 + h) * a.NS, a.NS, lane);
+        if (lane == 0) sm_lse[h] = all.x + log2f(all.y);
+    }
+    __syncthreads();
+    const int s1 = min(s0 + kFinishSlots, n);
+    for (int s = s0 + tid; s < s1; s += kFinishThreads) {
+        float w = 0.f;
+        for (int h = 0; h < a.G; ++h) w += ptx::ex2(a.scores[(unit * a.G + h) * a.S + s] - sm_lse[h]);
+        weights[unit * a.S + s] += w;
+    }
+}
+
+}  // namespace swa

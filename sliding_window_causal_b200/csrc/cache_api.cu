@@ -1,0 +1,377 @@
+// cache_api.cu: the C ABI of the caches beside the ring (include/swa.h): key weights, the budget
+// cache's seed, append and decode, and decoding behind a prefix that a whole batch shares.
+// Validates arguments and launches; every check is made before anything is enqueued.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdint>
+#include <cstdio>
+
+#include "api_internal.h"
+#include "attend.cuh"
+#include "cache.cuh"
+#include "keyweights.cuh"
+#include "swa.h"
+
+namespace {
+
+int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int fail(int code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    return swa_internal::set_error(code, buf);
+}
+int success() { return swa_internal::clear_error(); }
+int launched(const char* fn) {
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(SWA_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
+    return SWA_OK;
+}
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+constexpr int64_t kMaxGroup = 1024;  // query heads to a key head
+
+// Sizes shared by all entry points: each at least lo, the products inside 64-bit byte offsets.
+int check_heads(const char* fn, int64_t B, int64_t H, int64_t Hkv, int64_t D) {
+    if (B < 0 || H < 0 || Hkv < 0)
+        return fail(SWA_ERR_INVALID_ARG, "%s: negative size B=%lld H=%lld Hkv=%lld", fn, (long long)B, (long long)H,
+                    (long long)Hkv);
+    if (D < 1) return fail(SWA_ERR_INVALID_ARG, "%s: head dim D=%lld must be >= 1", fn, (long long)D);
+    if (H > 0 && (Hkv < 1 || H % Hkv != 0))
+        return fail(SWA_ERR_INVALID_ARG, "%s: H=%lld is not a multiple of Hkv=%lld", fn, (long long)H, (long long)Hkv);
+    if (B > INT32_MAX || H > INT32_MAX || (B > 0 && H > INT32_MAX / B))
+        return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    if (H > 0 && H / Hkv > kMaxGroup)
+        return fail(SWA_ERR_UNSUPPORTED, "%s: more than %lld query heads to a key head", fn, (long long)kMaxGroup);
+    return SWA_OK;
+}
+int check_head_dim(const char* fn, int64_t D) {
+    if (D != 64 && D != 128)
+        return fail(SWA_ERR_UNSUPPORTED, "%s: bf16 needs D = 64 or 128 (got %lld)", fn, (long long)D);
+    return SWA_OK;
+}
+// n operands' element strides, in[x] per dimension of size size[x] (dims of them); NULL = dense.
+int read_strides(const char* fn, const int64_t* in, int n, int dims, const int64_t* size, const int64_t* dense,
+                 int64_t mult, int64_t* out) {
+    for (int a = 0; a < n; ++a)
+        for (int x = 0; x < dims; ++x) {
+            int64_t v = in ? in[dims * a + x] : dense[x];
+            if (v < 0 || v > (int64_t(1) << 38))
+                return fail(SWA_ERR_INVALID_ARG, "%s: stride %lld of operand %d is negative or too large", fn,
+                            (long long)v, a);
+            if (size[x] == 1) v = dense[x];
+            if (v % mult != 0)
+                return fail(SWA_ERR_MISALIGNED, "%s: bf16 strides must be multiples of 8 elements (16 bytes); operand %d "
+                            "has stride %lld", fn, a, (long long)v);
+            out[dims * a + x] = v;
+        }
+    return SWA_OK;
+}
+
+cudaLaunchConfig_t config(dim3 grid, unsigned block, size_t smem, cudaStream_t s) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(block);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    return c;
+}
+// A launch that may start before the kernel ahead of it on the stream has ended; the kernel
+// itself waits (grid_dependency_wait).
+template <typename... P, typename... A>
+void launch_after(dim3 grid, unsigned block, size_t smem, cudaStream_t s, void (*kernel)(P...), A... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = config(grid, block, smem, s);
+    c.attrs = at;
+    c.numAttrs = 1;
+    cudaLaunchKernelEx(&c, kernel, args...);
+}
+
+// ------------------------------------------------------------------ decode over slots and prefix
+// Splits of one call. The sizes alone decide them (148 SMs assumed), so a workspace query and a
+// call always agree.
+struct Plan {
+    int ns, chunk;    // the streams' slots
+    int np, pchunk;   // the prefix
+    int64_t NS;
+    int64_t off_o, off_scores, bytes;  // workspace: (m, l), o, scores
+};
+
+void split(int64_t units, int64_t keys, int* n, int* chunk) {
+    const int64_t target = 148 * 8;
+    int64_t s = (target + units - 1) / units;
+    int64_t c = (keys + s - 1) / s;
+    c = (c + swa::kAttendStep - 1) / swa::kAttendStep * swa::kAttendStep;
+    *chunk = (int)c;
+    *n = (int)((keys + c - 1) / c);
+}
+
+int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
+
+Plan plan(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D, bool scores) {
+    Plan p = {};
+    const int64_t G = H / Hkv, Q = swa::kAttendQueries;
+    split(B * Hkv * ((G + Q - 1) / Q), S, &p.ns, &p.chunk);
+    if (P > 0) split(Hkv * ((B * G + Q - 1) / Q), P, &p.np, &p.pchunk);
+    p.NS = p.ns + p.np;
+    p.off_o = round256(B * H * p.NS * 8);
+    p.off_scores = p.off_o + round256(B * H * p.NS * D * 4);
+    p.bytes = p.off_scores + (scores ? round256(B * H * S * 4) : 0);
+    return p;
+}
+
+// Sizes that plan() can take: everything below 2^31 and every byte count far inside 64 bits.
+int check_decode_sizes(const char* fn, int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D) {
+    if (int rc = check_heads(fn, B, H, Hkv, D)) return rc;
+    if (S < 1) return fail(SWA_ERR_INVALID_ARG, "%s: %lld slots, at least 1 needed", fn, (long long)S);
+    if (P < 0) return fail(SWA_ERR_INVALID_ARG, "%s: negative prefix length %lld", fn, (long long)P);
+    if (B == 0 || H == 0) return SWA_OK;
+    if (int rc = check_head_dim(fn, D)) return rc;
+    if (S > INT32_MAX / 2 || P > INT32_MAX / 2 || B * H > (int64_t(1) << 28))
+        return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    return SWA_OK;
+}
+
+template <int D>
+void launch_decode(const Plan& pl, const swa::AttendArgs& ring, const swa::AttendArgs& pre, __nv_bfloat16* out,
+                   float* weights, cudaStream_t s) {
+    const int Q = swa::kAttendQueries;
+    const int64_t units = (int64_t)ring.B * ring.Hkv;
+    const unsigned threads = swa::kAttendWarps * 32;
+    if (pl.np > 0) {
+        const dim3 grid((unsigned)((int64_t)ring.Hkv * (((int64_t)ring.B * ring.G + Q - 1) / Q)), (unsigned)pl.np);
+        swa::attend_kernel<D, true, false><<<grid, threads, 0, s>>>(pre);
+    }
+    const dim3 grid((unsigned)(units * ((ring.G + Q - 1) / Q)), (unsigned)pl.ns);
+    if (weights) swa::attend_kernel<D, false, true><<<grid, threads, 0, s>>>(ring);
+    else swa::attend_kernel<D, false, false><<<grid, threads, 0, s>>>(ring);
+    const int slot_blocks = weights ? (ring.S + swa::kFinishSlots - 1) / swa::kFinishSlots : 0;
+    const int64_t blocks = (int64_t)ring.B * ring.H + units * slot_blocks;
+    launch_after(dim3((unsigned)blocks), swa::kFinishThreads, (size_t)ring.G * 4, s, swa::finish_kernel<D>, ring, out,
+                 weights, slot_blocks);
+}
+
+int decode(const char* fn, const void* q, const void* k, const void* v, const int64_t* pos, const void* kp, const void* vp,
+           float* weights, bool scores, void* out, void* workspace, int64_t workspace_bytes, int64_t B, int64_t H,
+           int64_t Hkv, int64_t S, int64_t P, int64_t D, double scale, const int64_t* strides, void* stream) {
+    if (int rc = check_decode_sizes(fn, B, H, Hkv, S, P, D)) return rc;
+    if (!std::isfinite(scale)) return fail(SWA_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    if (B == 0 || H == 0) return success();
+    if (!(scale > 0.0)) return fail(SWA_ERR_UNSUPPORTED, "%s: scale must be > 0 (got %g)", fn, scale);
+    if (!q || !k || !v || !pos || !out || !workspace || (scores && !weights) || (P > 0 && (!kp || !vp)))
+        return fail(SWA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    const Plan pl = plan(B, H, Hkv, S, P, D, scores);
+    if (workspace_bytes < pl.bytes)
+        return fail(SWA_ERR_INVALID_ARG, "%s: workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes,
+                    (long long)pl.bytes);
+    const void* p16[] = {q, k, v, out, P > 0 ? kp : nullptr, P > 0 ? vp : nullptr};
+    for (const void* x : p16)
+        if (!aligned(x, 16)) return fail(SWA_ERR_MISALIGNED, "%s: tensors must be 16-byte aligned", fn);
+    if (!aligned(workspace, 256) || !aligned(pos, 8) || (scores && !aligned(weights, 4)))
+        return fail(SWA_ERR_MISALIGNED, "%s: workspace must be 256-byte, pos 8-byte and weights 4-byte aligned", fn);
+    int64_t st[4] = {0, 0, 0, 0};
+    if (P > 0) {
+        const int64_t size[2] = {Hkv, P}, dense[2] = {P * D, D};
+        if (int rc = read_strides(fn, strides, 2, 2, size, dense, 8, st)) return rc;
+    }
+    const int64_t G = H / Hkv;
+    const int64_t blocks = B * H + (scores ? B * Hkv * ((S + swa::kFinishSlots - 1) / swa::kFinishSlots) : 0);
+    if (blocks > INT32_MAX || pl.ns > 65535 || pl.np > 65535) return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    int *status, num_sms;
+    if (int rc = swa_internal::device_info(&status, &num_sms)) return rc;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    swa::AttendArgs a = {};
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.pos = pos;
+    a.ml = reinterpret_cast<float2*>(ws);
+    a.o = reinterpret_cast<float*>(ws + pl.off_o);
+    a.scores = scores ? reinterpret_cast<float*>(ws + pl.off_scores) : nullptr;
+    a.k_head = a.v_head = S * D;
+    a.k_row = a.v_row = D;
+    a.B = (int)B;
+    a.H = (int)H;
+    a.Hkv = (int)Hkv;
+    a.G = (int)G;
+    a.S = (int)S;
+    a.chunk = pl.chunk;
+    a.split0 = pl.np;
+    a.NS = (int)pl.NS;
+    a.scale_log2 = (float)(1.4426950408889634 * scale);
+    a.status = status;
+    swa::AttendArgs pre = a;
+    pre.k = static_cast<const __nv_bfloat16*>(kp);
+    pre.v = static_cast<const __nv_bfloat16*>(vp);
+    pre.k_head = st[0];
+    pre.k_row = st[1];
+    pre.v_head = st[2];
+    pre.v_row = st[3];
+    pre.S = (int)P;
+    pre.chunk = pl.pchunk;
+    pre.split0 = 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto* ob = static_cast<__nv_bfloat16*>(out);
+    float* w = scores ? weights : nullptr;
+    if (D == 128) launch_decode<128>(pl, a, pre, ob, w, s);
+    else launch_decode<64>(pl, a, pre, ob, w, s);
+    if (int rc = launched(fn)) return rc;
+    return success();
+}
+
+int64_t decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D, bool scores) {
+    if (check_decode_sizes("workspace size", B, H, Hkv, S, P, D)) return -1;
+    if (B == 0 || H == 0) return 0;
+    return plan(B, H, Hkv, S, P, D, scores).bytes;
+}
+
+}  // namespace
+
+extern "C" {
+
+int swa_key_weights(const void* q, const void* k, const float* lse, const int64_t* lens, float* weights, int64_t B,
+                    int64_t H, int64_t Hkv, int64_t T, int64_t D, int64_t W, int64_t last, double scale,
+                    const int64_t* strides, int dtype, void* stream) {
+    const char* fn = "swa_key_weights";
+    if (dtype != SWA_F32 && dtype != SWA_BF16)
+        return fail(SWA_ERR_INVALID_ARG, "%s: dtype %d is neither SWA_F32 nor SWA_BF16", fn, dtype);
+    if (int rc = check_heads(fn, B, H, Hkv, D)) return rc;
+    if (T < 0) return fail(SWA_ERR_INVALID_ARG, "%s: negative size T=%lld", fn, (long long)T);
+    if (W < 1) return fail(SWA_ERR_INVALID_ARG, "%s: window W=%lld must be >= 1", fn, (long long)W);
+    if (last < 1) return fail(SWA_ERR_INVALID_ARG, "%s: last=%lld must be >= 1", fn, (long long)last);
+    if (!std::isfinite(scale)) return fail(SWA_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    if (B == 0 || H == 0 || T == 0) return success();
+    if (!q || !k || !lse || !weights) return fail(SWA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (dtype == SWA_BF16) {
+        if (int rc = check_head_dim(fn, D)) return rc;
+    } else if (D > 4096) {
+        return fail(SWA_ERR_UNSUPPORTED, "%s: fp32 supports D <= 4096", fn);
+    }
+    const int64_t n_kt = (T + swa::kKwTile - 1) / swa::kKwTile;
+    if (T > INT32_MAX / 2 || B * Hkv > INT32_MAX / n_kt) return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    const size_t al = dtype == SWA_BF16 ? 16 : 4;
+    if (!aligned(q, al) || !aligned(k, al))
+        return fail(SWA_ERR_MISALIGNED, "%s: q and k must be %d-byte aligned", fn, (int)al);
+    if (!aligned(lse, 4) || !aligned(weights, 4) || !aligned(lens, 8))
+        return fail(SWA_ERR_MISALIGNED, "%s: lse and weights must be 4-byte and lens 8-byte aligned", fn);
+    int64_t qs[3], ks[3];
+    {
+        const int64_t size[3] = {B, H, T}, dense[3] = {H * T * D, T * D, D};
+        if (int rc = read_strides(fn, strides, 1, 3, size, dense, dtype == SWA_BF16 ? 8 : 1, qs)) return rc;
+        const int64_t ksize[3] = {B, Hkv, T}, kdense[3] = {Hkv * T * D, T * D, D};
+        if (int rc = read_strides(fn, strides ? strides + 3 : nullptr, 1, 3, ksize, kdense, dtype == SWA_BF16 ? 8 : 1, ks))
+            return rc;
+    }
+    const int Wi = (int)(W < T ? W : T), Li = (int)(last < T ? last : T);
+    int *status, num_sms;
+    if (int rc = swa_internal::device_info(&status, &num_sms)) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned grid = (unsigned)(B * Hkv * n_kt);
+    auto run = [&](auto* qp, auto* kp) {
+        swa::key_weights_simt_kernel<<<grid, 256, 0, s>>>(qp, kp, lse, lens, weights, qs[0], qs[1], qs[2], ks[0], ks[1],
+                                                          ks[2], (int)H, (int)Hkv, (int)T, (int)D, Wi, Li, (float)scale,
+                                                          (int)n_kt, status);
+    };
+    if (dtype == SWA_BF16) run(static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k));
+    else run(static_cast<const float*>(q), static_cast<const float*>(k));
+    if (int rc = launched(fn)) return rc;
+    return success();
+}
+
+int swa_cache_seed(const void* k, const void* v, const float* weights, const int64_t* lens, void* kcache, void* vcache,
+                   float* wcache, int64_t* pcache, int64_t B, int64_t Hkv, int64_t T, int64_t D, int64_t S, int64_t recent,
+                   const int64_t* strides, void* stream) {
+    const char* fn = "swa_cache_seed";
+    if (int rc = check_heads(fn, B, Hkv, Hkv, D)) return rc;
+    if (T < 0) return fail(SWA_ERR_INVALID_ARG, "%s: negative size T=%lld", fn, (long long)T);
+    if (S < 1) return fail(SWA_ERR_INVALID_ARG, "%s: %lld slots, at least 1 needed", fn, (long long)S);
+    if (recent < 0 || recent >= S)
+        return fail(SWA_ERR_INVALID_ARG, "%s: recent=%lld must be in [0, %lld)", fn, (long long)recent, (long long)S);
+    if (B == 0 || Hkv == 0 || T == 0) return success();
+    if (!k || !v || !weights || !kcache || !vcache || !wcache || !pcache)
+        return fail(SWA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (int rc = check_head_dim(fn, D)) return rc;
+    if (T > INT32_MAX / 2 || S > INT32_MAX / 2) return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kcache, 16) || !aligned(vcache, 16))
+        return fail(SWA_ERR_MISALIGNED, "%s: key and value tensors must be 16-byte aligned", fn);
+    if (!aligned(weights, 4) || !aligned(wcache, 4) || !aligned(pcache, 8) || !aligned(lens, 8))
+        return fail(SWA_ERR_MISALIGNED, "%s: weights must be 4-byte, positions and lens 8-byte aligned", fn);
+    int64_t st[6];
+    const int64_t size[3] = {B, Hkv, T}, dense[3] = {Hkv * T * D, T * D, D};
+    if (int rc = read_strides(fn, strides, 2, 3, size, dense, 8, st)) return rc;
+    int *status, num_sms;
+    if (int rc = swa_internal::device_info(&status, &num_sms)) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    swa::seed_select_kernel<<<(unsigned)(B * Hkv), swa::kSeedThreads, 0, s>>>(weights, lens, wcache, pcache, (int)Hkv,
+                                                                             (int)T, (int)S, (int)recent, status);
+    if (int rc = launched(fn)) return rc;
+    const int vpr = (int)(D / 8);
+    const int64_t n_vec = B * Hkv * S * vpr;
+    int64_t blocks = (n_vec + 255) / 256;
+    if (blocks > 148 * 32) blocks = 148 * 32;
+    launch_after(dim3((unsigned)blocks), 256, 0, s, swa::seed_gather_kernel, static_cast<const __nv_bfloat16*>(k),
+                 static_cast<const __nv_bfloat16*>(v), lens, static_cast<const int64_t*>(pcache),
+                 static_cast<uint4*>(kcache), static_cast<uint4*>(vcache), st[0], st[1], st[2], st[3], st[4], st[5],
+                 (int)Hkv, (int)T, (int)S, vpr, n_vec);
+    if (int rc = launched(fn)) return rc;
+    return success();
+}
+
+int swa_cache_append(const void* k, const void* v, void* kcache, void* vcache, float* wcache, int64_t* pcache,
+                     const int64_t* pos, int64_t* slots, int64_t B, int64_t Hkv, int64_t D, int64_t S, int64_t recent,
+                     void* stream) {
+    const char* fn = "swa_cache_append";
+    if (int rc = check_heads(fn, B, Hkv, Hkv, D)) return rc;
+    if (S < 1) return fail(SWA_ERR_INVALID_ARG, "%s: %lld slots, at least 1 needed", fn, (long long)S);
+    if (recent < 0 || recent >= S)
+        return fail(SWA_ERR_INVALID_ARG, "%s: recent=%lld must be in [0, %lld)", fn, (long long)recent, (long long)S);
+    if (B == 0 || Hkv == 0) return success();
+    if (!k || !v || !kcache || !vcache || !wcache || !pcache || !pos || !slots)
+        return fail(SWA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (int rc = check_head_dim(fn, D)) return rc;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kcache, 16) || !aligned(vcache, 16))
+        return fail(SWA_ERR_MISALIGNED, "%s: key and value tensors must be 16-byte aligned", fn);
+    if (!aligned(wcache, 4) || !aligned(pcache, 8) || !aligned(pos, 8) || !aligned(slots, 8))
+        return fail(SWA_ERR_MISALIGNED, "%s: weights must be 4-byte, positions and slots 8-byte aligned", fn);
+    if (S > INT32_MAX / 2) return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    int *status, num_sms;
+    if (int rc = swa_internal::device_info(&status, &num_sms)) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    swa::cache_append_kernel<<<(unsigned)(B * Hkv), 256, 0, s>>>(
+        static_cast<const uint4*>(k), static_cast<const uint4*>(v), static_cast<uint4*>(kcache),
+        static_cast<uint4*>(vcache), wcache, pcache, pos, slots, (int)Hkv, (int)S, (int)recent, (int)(D / 8), status);
+    if (int rc = launched(fn)) return rc;
+    return success();
+}
+
+int64_t swa_cache_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D) {
+    return decode_workspace_bytes(B, H, Hkv, S, P, D, true);
+}
+
+int swa_cache_decode(const void* q, const void* kcache, const void* vcache, float* wcache, const int64_t* pos,
+                     const void* kprefix, const void* vprefix, void* out, void* workspace, int64_t workspace_bytes,
+                     int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D, double scale,
+                     const int64_t* strides, void* stream) {
+    return decode("swa_cache_decode", q, kcache, vcache, pos, kprefix, vprefix, wcache, true, out, workspace,
+                  workspace_bytes, B, H, Hkv, S, P, D, scale, strides, stream);
+}
+
+int64_t swa_prefix_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t W, int64_t P, int64_t D) {
+    return decode_workspace_bytes(B, H, Hkv, W, P, D, false);
+}
+
+int swa_prefix_decode(const void* q, const void* kprefix, const void* vprefix, const void* kring, const void* vring,
+                      const int64_t* pos, void* out, void* workspace, int64_t workspace_bytes, int64_t B, int64_t H,
+                      int64_t Hkv, int64_t W, int64_t P, int64_t D, double scale, const int64_t* strides, void* stream) {
+    return decode("swa_prefix_decode", q, kring, vring, pos, kprefix, vprefix, nullptr, false, out, workspace,
+                  workspace_bytes, B, H, Hkv, W, P, D, scale, strides, stream);
+}
+
+}  // extern "C"

@@ -35,6 +35,9 @@ struct DecodeCfg {
     static constexpr int kRowsPerBatch = kDecodeWarps * kRowsPerStep * kDecodeUnroll;
 };
 
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
 __device__ __forceinline__ uint4 ld_stream_16(const void* p) {
     uint4 r;
     asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"

@@ -1123,4 +1123,12 @@ int clear_error() {
     t_error.clear();
     return SWA_OK;
 }
+int device_info(int** status, int* num_sms) {
+    DeviceState* ds;
+    if (int rc = device_state(&ds)) return rc;
+    *status = ds->status;
+    *num_sms = ds->num_sms;
+    return SWA_OK;
+}
+uint64_t wait_limit_ns() { return wait_limit(); }
 }  // namespace swa_internal

@@ -17,14 +17,12 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "decode.cuh"
 #include "prefill_simt.cuh"
 
 namespace swa {
 
 constexpr int kWeightWarps = 4;
-
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 // Dynamic shared memory: per warp q[D] floats. qs, ks: (b, h, t) element strides.
 template <typename TIn>
