@@ -2,6 +2,7 @@
 // include/swa.h). The message set here is what swa_last_error() returns.
 #pragma once
 
+#include <cuda.h>
 #include <stdint.h>
 
 namespace swa_internal {
@@ -20,4 +21,8 @@ int check_forward(const char* fn, const void* q, const void* k, const void* v, c
 int device_info(int** status, int* num_sms);
 // The time limit of the kernels' bounded waits, in nanoseconds.
 uint64_t wait_limit_ns();
+// The TMA map of a bf16 [B, H, T, D] tensor with element strides st = (b, h, t): boxes of 64
+// columns x `rows` rows of one (b, h), 128-byte swizzle, rows past T zero.
+int tensor_map(CUtensorMap* m, const void* ptr, int64_t B, int64_t H, int64_t T, int64_t D, const int64_t st[3],
+               int rows);
 }  // namespace swa_internal

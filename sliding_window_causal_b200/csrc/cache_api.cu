@@ -8,6 +8,9 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <mutex>
+#include <set>
+#include <utility>
 
 #include "api_internal.h"
 #include "attend.cuh"
@@ -92,6 +95,51 @@ void launch_after(dim3 grid, unsigned block, size_t smem, cudaStream_t s, void (
     c.attrs = at;
     c.numAttrs = 1;
     cudaLaunchKernelEx(&c, kernel, args...);
+}
+
+// Let `kernel` use `bytes` of dynamic shared memory on the current device (once a device).
+int allow_smem(const void* kernel, int bytes) {
+    static std::mutex mu;
+    static std::set<std::pair<int, const void*>> done;
+    int dev;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail(SWA_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    std::lock_guard<std::mutex> lk(mu);
+    if (done.count({dev, kernel})) return SWA_OK;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return fail(SWA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    done.insert({dev, kernel});
+    return SWA_OK;
+}
+
+// ------------------------------------------------------------------ key weights
+template <int D>
+int launch_key_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const float* lse, const int64_t* lens,
+                       float* weights, int64_t B, int64_t H, int64_t Hkv, int64_t T, int W, int last, double scale,
+                       int* status, cudaStream_t s) {
+    auto* kernel = swa::key_weights_tc_kernel<D>;
+    if (int rc = allow_smem(reinterpret_cast<const void*>(kernel), swa::KwCfg<D>::kSmemBytes)) return rc;
+    const int64_t tiles = (T + 127) / 128;
+    // A cluster splits a key tile's query slices while the working CTAs (the tiles that some
+    // counted query sees, at most) do not fill the 148 SMs twice and each keeps 4 slices or more.
+    const int64_t seen = (int64_t)W + last < T ? (int64_t)W + last : T;
+    const int64_t work = B * Hkv * ((seen + 127) / 128);
+    const int64_t rows = 127 + (int64_t)(W < last ? W : last);
+    const int64_t slices = H / Hkv * ((rows + swa::kKwSlice - 1) / swa::kKwSlice);
+    int C = 1;
+    while (C < 8 && work * C < 2 * 148 && slices >= 8 * C) C *= 2;
+    const int64_t grid = B * Hkv * tiles * C;
+    if (grid > INT32_MAX) C = 1;
+    cudaLaunchConfig_t cfg = config(dim3((unsigned)(B * Hkv * tiles * C)), swa::kKwThreads, swa::KwCfg<D>::kSmemBytes, s);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)C;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    cudaLaunchKernelEx(&cfg, kernel, tm_q, tm_k, lse, lens, weights, (int)H, (int)Hkv, (int)T, W, last,
+                       (float)(1.4426950408889634 * scale), C, swa_internal::wait_limit_ns(), status);
+    return SWA_OK;
 }
 
 // ------------------------------------------------------------------ decode over slots and prefix
@@ -273,14 +321,18 @@ int swa_key_weights(const void* q, const void* k, const float* lse, const int64_
     int *status, num_sms;
     if (int rc = swa_internal::device_info(&status, &num_sms)) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)(B * Hkv * n_kt);
-    auto run = [&](auto* qp, auto* kp) {
-        swa::key_weights_simt_kernel<<<grid, 256, 0, s>>>(qp, kp, lse, lens, weights, qs[0], qs[1], qs[2], ks[0], ks[1],
-                                                          ks[2], (int)H, (int)Hkv, (int)T, (int)D, Wi, Li, (float)scale,
-                                                          (int)n_kt, status);
-    };
-    if (dtype == SWA_BF16) run(static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k));
-    else run(static_cast<const float*>(q), static_cast<const float*>(k));
+    if (dtype == SWA_BF16) {
+        CUtensorMap tm_q, tm_k;
+        if (int rc = swa_internal::tensor_map(&tm_q, q, B, H, T, D, qs, swa::kKwSlice)) return rc;
+        if (int rc = swa_internal::tensor_map(&tm_k, k, B, Hkv, T, D, ks, 128)) return rc;
+        if (int rc = D == 128 ? launch_key_weights<128>(tm_q, tm_k, lse, lens, weights, B, H, Hkv, T, Wi, Li, scale, status, s)
+                              : launch_key_weights<64>(tm_q, tm_k, lse, lens, weights, B, H, Hkv, T, Wi, Li, scale, status, s))
+            return rc;
+    } else {
+        swa::key_weights_simt_kernel<<<(unsigned)(B * Hkv * n_kt), 256, 0, s>>>(
+            static_cast<const float*>(q), static_cast<const float*>(k), lse, lens, weights, qs[0], qs[1], qs[2], ks[0],
+            ks[1], ks[2], (int)H, (int)Hkv, (int)T, (int)D, Wi, Li, (float)scale, (int)n_kt, status);
+    }
     if (int rc = launched(fn)) return rc;
     return success();
 }

@@ -217,14 +217,14 @@ EncodeTiledFn encode_fn() {
 
 // A bf16 [B, H, T, D] tensor with element strides st = (b, h, t) (D contiguous), viewed as
 // the 4-D tensor {D, T, H, B}: boxes of 64 columns x 128 rows of one (b, h), 128-byte
-// swizzle. Rows past T read as zeros.
+// swizzle. Rows past T read as zeros. (rows: another number of rows to a box.)
 int make_map(CUtensorMap* m, const void* ptr, int64_t B, int64_t H, int64_t T, int64_t D,
-             const int64_t st[3]) {
+             const int64_t st[3], int rows = 128) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return fail(SWA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
     cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)H, (cuuint64_t)B};
     cuuint64_t strides[3] = {(cuuint64_t)(st[2] * 2), (cuuint64_t)(st[1] * 2), (cuuint64_t)(st[0] * 2)};
-    cuuint32_t box[4] = {64, 128, 1, 1};
+    cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides,
                      box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1131,4 +1131,8 @@ int device_info(int** status, int* num_sms) {
     return SWA_OK;
 }
 uint64_t wait_limit_ns() { return wait_limit(); }
+int tensor_map(CUtensorMap* m, const void* ptr, int64_t B, int64_t H, int64_t T, int64_t D, const int64_t st[3],
+               int rows) {
+    return make_map(m, ptr, B, H, T, D, st, rows);
+}
 }  // namespace swa_internal
