@@ -303,7 +303,7 @@ int swa_key_weights(const void* q, const void* k, const float* lse, const int64_
         return fail(SWA_ERR_UNSUPPORTED, "%s: fp32 supports D <= 4096", fn);
     }
     const int64_t n_kt = (T + swa::kKwTile - 1) / swa::kKwTile;
-    if (T > INT32_MAX / 2 || B * Hkv > INT32_MAX / n_kt) return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    if (T > (int64_t(1) << 29) || B * Hkv > INT32_MAX / n_kt) return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     const size_t al = dtype == SWA_BF16 ? 16 : 4;
     if (!aligned(q, al) || !aligned(k, al))
         return fail(SWA_ERR_MISALIGNED, "%s: q and k must be %d-byte aligned", fn, (int)al);

@@ -96,22 +96,22 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ bf16, tensor cores
 // key_weights_tc_kernel: a CTA owns 128 keys, the rows of S^T = K Q^T, so that a thread's TMEM
 // lane is a key and its sum needs no exchange: no maximum, no second product, no atomics. The
-// queries that see the tile's keys come in slices of 64 rows (head gh of the group, rows i0 ..),
-// two to a stage of 128 columns. Roles:
-//   warp 0, lane 0   TMA producer: the key tile, then the query slices through a ring
-//   warp 1           TMEM allocation and MMA issue; S^T double buffered (256 columns)
-//   warp 2           -lse log2(e) of each stage's columns into shared memory
-//   warps 3 .. 10    p = 2^(s c + nlse) and the row sums: warp = (TMEM quarter, slice)
-// Bound: one exp a band pair against 2 D tensor-core flops. The special-function unit alone
-// would take 2 x the MMA's time at D = 128, so kKwPolyOf8 of each 8 exponentials are computed
-// on the FMA pipe (kw_exp2_parts). Two CTAs share an SM (88 registers a thread, 256 TMEM
-// columns, about 100 KB of shared memory), so that one's start and end overlap the other's work.
-// Few keys and many queries: a cluster of C CTAs splits the slices of one key tile and adds its
-// sums in rank order through distributed shared memory.
-constexpr int kKwThreads = 352;
-constexpr int kKwSlice = 64;     // query rows of a slice
-constexpr int kKwStats = 4;      // stages of nlse in shared memory
-constexpr int kKwPolyOf8 = 4;    // column pairs of each 8 whose exponentials use the FMA pipe
+// queries that see the tile's keys come in slices of 64 rows (a head of the group, rows i0 ..),
+// two to a stage of 128 columns. Stage j uses ring slot, TMEM buffer and warpgroup j & 1. Roles:
+//   warp 0        TMA of the key tile and the query slices (lane 0); -lse log2(e) of each stage's
+//                 columns into shared memory
+//   warp 1        TMEM allocation and MMA issue
+//   warps 2 .. 9  two warpgroups: p = 2^(s c + nlse) and the row sums of every second stage
+// Bound: one exp a band pair on the special-function unit (16 a clock and SM), 2 x the time of
+// the product at D = 128. 32 heads of 16384 tokens, W 4096 (1.88 G exponentials): 582 us, 0.72
+// of that unit's rate; with 1, 2, 3 or 4 of each 8 exponentials as a polynomial on the FMA pipe
+// 588, 614, 665 and 681 us, as the warps' issue slots run out first. Two CTAs share an SM, so
+// that one's start and end overlap the other's work. Few keys and many queries: a cluster of C
+// CTAs splits the slices of one key tile and adds its sums in rank order through distributed
+// shared memory.
+constexpr int kKwThreads = 320;
+constexpr int kKwSlice = 64;  // query rows of a slice
+constexpr int kKwStats = 8;   // stages of nlse in shared memory
 
 template <int D>
 struct KwCfg {
@@ -119,41 +119,15 @@ struct KwCfg {
     static constexpr int kBoxBytes = 128 * 128;  // 128 rows x 64 bf16
     static constexpr int kTileBytes = 128 * D * 2;
     static constexpr int kSliceBytes = kTileBytes / 2;
-    static constexpr int kStages = D == 128 ? 2 : 4;
     static constexpr int kRingOff = kTileBytes;
-    static constexpr int kNlOff = kRingOff + kStages * kTileBytes;
-    static constexpr int kRedOff = kNlOff + kKwStats * 128 * 4;  // [2][128] sums of the two slices
+    static constexpr int kNlOff = kRingOff + 2 * kTileBytes;
+    static constexpr int kRedOff = kNlOff + kKwStats * 128 * 4;  // [2][128] sums of the two warpgroups
     static constexpr int kBarOff = kRedOff + 2 * 128 * 4;
-    // k_full, ring_full[NS], ring_empty[NS], s_full[2], s_read[2], nl_full[4], nl_free[4], drain
-    static constexpr int kNumBars = 2 + 2 * kStages + 4 + 2 * kKwStats;
+    static constexpr int kNumBars = 8;  // k_full, ring_full[2], s_full[2], s_read[2], drain
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
     static constexpr uint32_t kTmemCols = 256;
 };
-
-// 2^z of two values, as p * 2^n with n = round(z) and p = 2^(z - n), |z - n| <= 1/2. p is the
-// polynomial of degree 5 that interpolates 2^f at the Chebyshev nodes of [-1/2, 1/2]: off by at
-// most 1.1e-7 of it there, 2.4e-7 with fp32 coefficients and steps. z is held in [-126, 128] (2^128 is
-// infinity in fp32); NaN stays NaN.
-__device__ __forceinline__ float kw_clamp(float z) {
-    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(z));  // -126
-    asm("min.NaN.f32 %0, %0, 0f43000000;" : "+f"(z));  // 128
-    return z;
-}
-__device__ __forceinline__ void kw_exp2_parts(ptx::f32x2 z, ptx::f32x2& p, ptx::f32x2& pow2) {
-    const ptx::f32x2 magic = {12582912.f, 12582912.f};  // 1.5 * 2^23: its sum with z ends in round(z)
-    z = {kw_clamp(z.x), kw_clamp(z.y)};
-    const ptx::f32x2 t = ptx::add2(z, magic);
-    const ptx::f32x2 f = ptx::sub2(z, ptx::sub2(t, magic));
-    p = {0.00133908633f, 0.00133908633f};
-    p = ptx::fma2(p, f, {0.00967603177f, 0.00967603177f});
-    p = ptx::fma2(p, f, {0.0555035695f, 0.0555035695f});
-    p = ptx::fma2(p, f, {0.240221068f, 0.240221068f});
-    p = ptx::fma2(p, f, {0.693147182f, 0.693147182f});
-    p = ptx::fma2(p, f, {1.00000012f, 1.00000012f});
-    pow2 = {__uint_as_float(__float_as_uint(t.x) * 0x00800000u + 0x3F800000u),
-            __uint_as_float(__float_as_uint(t.y) * 0x00800000u + 0x3F800000u)};
-}
 
 // What a CTA works on.
 struct KwItem {
@@ -165,29 +139,23 @@ struct KwItem {
     __device__ __forceinline__ int row(int s) const { return i_lo + kKwSlice * (s % per_head); }
 };
 
-// Sums of 32 columns of a row: v scores, nl the columns' nlse; EDGE: only columns
-// cmin .. cmax count.
+// Sums of 16 columns of a row: v scores, nl the columns' nlse; EDGE: only those whose bit of
+// mask is set count.
 template <bool EDGE>
-__device__ __forceinline__ void kw_sum32(const uint32_t (&v)[32], const float* nl, float c2, int cmin, int cmax,
+__device__ __forceinline__ void kw_sum16(const uint32_t (&v)[16], const float* nl, float c2, uint32_t mask,
                                          ptx::f32x2 (&acc)[2]) {
     const ptx::f32x2 cc = {c2, c2};
 #pragma unroll
-    for (int t = 0; t < 32; t += 4) {
+    for (int t = 0; t < 16; t += 4) {
         const float4 n4 = *reinterpret_cast<const float4*>(nl + t);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int x = t + 2 * u;
-            ptx::f32x2 z = ptx::fma2({__uint_as_float(v[x]), __uint_as_float(v[x + 1])}, cc,
-                                     u ? ptx::f32x2{n4.z, n4.w} : ptx::f32x2{n4.x, n4.y});
-            const bool in0 = !EDGE || (x >= cmin && x <= cmax), in1 = !EDGE || (x + 1 >= cmin && x + 1 <= cmax);
-            if (!EDGE && (x / 2) % 8 % 2 == 0 && (x / 2) % 8 / 2 < kKwPolyOf8) {
-                ptx::f32x2 p, e;
-                kw_exp2_parts(z, p, e);
-                acc[u] = ptx::fma2(p, e, acc[u]);
-            } else {
-                const ptx::f32x2 p = {ptx::ex2(z.x), ptx::ex2(z.y)};
-                acc[u] = ptx::add2(acc[u], {in0 ? p.x : 0.f, in1 ? p.y : 0.f});
-            }
+            const ptx::f32x2 z = ptx::fma2({__uint_as_float(v[x]), __uint_as_float(v[x + 1])}, cc,
+                                           u ? ptx::f32x2{n4.z, n4.w} : ptx::f32x2{n4.x, n4.y});
+            ptx::f32x2 p = {ptx::ex2(z.x), ptx::ex2(z.y)};
+            if (EDGE) p = {mask & (1u << x) ? p.x : 0.f, mask & (2u << x) ? p.y : 0.f};
+            acc[u] = ptx::add2(acc[u], p);
         }
     }
 }
@@ -198,17 +166,13 @@ __global__ void __launch_bounds__(kKwThreads, 2)
                           const float* __restrict__ lse, const int64_t* __restrict__ lens, float* __restrict__ out,
                           int H, int Hkv, int T, int W, int last, float c2, int C, uint64_t wait_limit_ns, int* status) {
     using Cf = KwCfg<D>;
-    constexpr int NS = Cf::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Cf::kBarOff);
-    uint64_t* ring_full = k_full + 1;        // [NS]
-    uint64_t* ring_empty = ring_full + NS;   // [NS]
-    uint64_t* s_full = ring_empty + NS;      // [2]
-    uint64_t* s_read = s_full + 2;           // [2] the scores of a buffer are in registers
-    uint64_t* nl_full = s_read + 2;          // [kKwStats]
-    uint64_t* nl_free = nl_full + kKwStats;  // [kKwStats]
-    uint64_t* drain = nl_free + kKwStats;
+    uint64_t* ring_full = k_full + 1;   // [2]
+    uint64_t* s_full = ring_full + 2;   // [2] the scores of a stage (and so its ring slot is free), and its nlse
+    uint64_t* s_read = s_full + 2;      // [2] the scores of a buffer are in registers
+    uint64_t* drain = s_read + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cf::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cf::kMiscOff + 4);
     float* sm_nl = reinterpret_cast<float*>(smem + Cf::kNlOff);
@@ -225,7 +189,7 @@ __global__ void __launch_bounds__(kKwThreads, 2)
         it.j0 = (int)(unit / BHk) * 128;
         it.n = stream_len(lens, it.b, T, status);
         it.i_lo = max(it.j0, it.n - last);
-        it.i_hi = (int)min((int64_t)it.n - 1, (int64_t)it.j0 + 127 + W - 1);
+        it.i_hi = min(it.n - 1, it.j0 + 127 + W - 1);  // T and W are at most 2^29
         const int rows = it.j0 < it.n ? it.i_hi - it.i_lo + 1 : 0;
         it.per_head = rows > 0 ? (rows + kKwSlice - 1) / kKwSlice : 0;
         const int64_t all = (int64_t)it.per_head * (H / Hkv);
@@ -233,22 +197,15 @@ __global__ void __launch_bounds__(kKwThreads, 2)
         it.s1 = (int)(all * (rank + 1) / C);
     }
     const int slices = it.s1 - it.s0, stages = (slices + 1) / 2;
-    float sum = 0.f;  // element-wise threads: the sum of this thread's row over its slices
+    float sum = 0.f;  // element-wise threads: the sum of this thread's row over its stages
 
     if (slices > 0) {  // uniform in the CTA
         if (tid == 0) {
             ptx::mbar_init(k_full, 1);
-            for (int s = 0; s < NS; ++s) {
-                ptx::mbar_init(ring_full + s, 1);
-                ptx::mbar_init(ring_empty + s, 1);
-            }
             for (int x = 0; x < 2; ++x) {
-                ptx::mbar_init(s_full + x, 1);
-                ptx::mbar_init(s_read + x, 8);
-            }
-            for (int x = 0; x < kKwStats; ++x) {
-                ptx::mbar_init(nl_full + x, 1);
-                ptx::mbar_init(nl_free + x, 8);
+                ptx::mbar_init(ring_full + x, 1);
+                ptx::mbar_init(s_full + x, 2);
+                ptx::mbar_init(s_read + x, 4);
             }
             ptx::mbar_init(drain, 1);
             *abort_flag = 0;
@@ -264,35 +221,68 @@ __global__ void __launch_bounds__(kKwThreads, 2)
         __syncthreads();
         ptx::tc_fence_after();
         const uint32_t tmem = *tmem_slot;
-        uint32_t loads = 0;  // producer: ring stages issued
+        uint32_t loads = 0;  // warp 0: stages whose loads are issued
 
         if (warp == 0) {
+            // ---------------------------------------------------------------- loads, nlse
             if (lane == 0) {
-                // ------------------------------------------------------------ producer
-                bool ok = true;
                 ptx::mbar_arrive_expect_tx(k_full, Cf::kTileBytes);
                 for (int c = 0; c < D / 64; ++c)
                     ptx::tma_load_4d(smem + c * Cf::kBoxBytes, &tm_k, k_full, 64 * c, it.j0, (int)it.hk, (int)it.b);
-                for (int j = 0; j < stages && ok; ++j) {
-                    const uint32_t st = loads % NS;
-                    if (loads >= (uint32_t)NS)
-                        ok = ptx::mbar_wait(ring_empty + st, ((loads / NS) - 1) & 1, wait_limit_ns, abort_flag);
+            }
+            bool ok = true;
+            // the lse of a stage are read two stages before they are stored
+            float a[2][4];
+            auto fetch = [&](int j, float (&r)[4]) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int s = it.s0 + 2 * j + x;
+                    r[2 * x] = r[2 * x + 1] = INFINITY;
+                    if (s < it.s1) {
+                        const int i = it.row(s) + lane;
+                        const float* p = lse + ((int64_t)it.b * H + it.hk * (H / Hkv) + it.head(s)) * T + i;
+                        if (i <= it.i_hi) r[2 * x] = p[0];
+                        if (i + 32 <= it.i_hi) r[2 * x + 1] = p[32];
+                    }
+                }
+            };
+            fetch(0, a[0]);
+            fetch(1, a[1]);
+            for (int j0 = 0; j0 < stages && ok; j0 += 2) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int j = j0 + y;
+                    if (j >= stages || !ok) break;
+                    // Stage j - 2 has its scores: ring slot y is free, and so is the nlse slot of
+                    // stage j - 8: those scores were computed after the warpgroup had read stage
+                    // j - 4's, which it does after it has finished stage j - 6.
+                    if (j >= 2)
+                        ok = __all_sync(0xffffffffu,
+                                        ptx::mbar_wait(s_full + y, ((j >> 1) - 1) & 1, wait_limit_ns, abort_flag));
                     if (!ok) break;
-                    uint8_t* dst = smem + Cf::kRingOff + st * Cf::kTileBytes;
-                    const int here = min(2, slices - 2 * j);
-                    ptx::mbar_arrive_expect_tx(ring_full + st, here * Cf::kSliceBytes);
-                    for (int x = 0; x < here; ++x) {
-                        const int s = it.s0 + 2 * j + x;
-                        for (int c = 0; c < D / 64; ++c)
-                            ptx::tma_load_4d(dst + c * Cf::kBoxBytes + x * (Cf::kBoxBytes / 2), &tm_q, ring_full + st,
-                                             64 * c, it.row(s), (int)it.hk * (H / Hkv) + it.head(s), (int)it.b);
+                    if (lane == 0) {
+                        uint8_t* dst = smem + Cf::kRingOff + y * Cf::kTileBytes;
+                        const int here = min(2, slices - 2 * j);
+                        ptx::mbar_arrive_expect_tx(ring_full + y, here * Cf::kSliceBytes);
+                        for (int x = 0; x < here; ++x) {
+                            const int s = it.s0 + 2 * j + x;
+                            for (int c = 0; c < D / 64; ++c)
+                                ptx::tma_load_4d(dst + c * Cf::kBoxBytes + x * (Cf::kBoxBytes / 2), &tm_q, ring_full + y,
+                                                 64 * c, it.row(s), (int)it.hk * (H / Hkv) + it.head(s), (int)it.b);
+                        }
                     }
                     ++loads;
+                    float* nl = sm_nl + 128 * (j % kKwStats) + lane;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) nl[32 * x] = a[y][x] * -1.4426950408889634f;
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(s_full + y);
+                    fetch(j + 2, a[y]);
                 }
-                if (!ok) {
-                    atomicCAS(status, 0, 5);
-                    *abort_flag = 1;
-                }
+            }
+            if (!ok && lane == 0) {
+                atomicCAS(status, 0, 5);
+                *abort_flag = 1;
             }
         } else if (warp == 1) {
             // ---------------------------------------------------------------- MMA issuer
@@ -304,61 +294,20 @@ __global__ void __launch_bounds__(kKwThreads, 2)
             const uint32_t k_lo = (ptx::smem_u32(smem) >> 4) | lo;
             bool ok = wait(k_full, 0);
             for (int j = 0; j < stages && ok; ++j) {
-                const uint32_t st = j % NS, buf = j & 1;
-                if (j >= 2) ok = wait(s_read + buf, ((j >> 1) - 1) & 1);
-                if (ok) ok = wait(ring_full + st, (j / NS) & 1);
+                const uint32_t y = j & 1;
+                if (j >= 2) ok = wait(s_read + y, ((j >> 1) - 1) & 1);
+                if (ok) ok = wait(ring_full + y, (j >> 1) & 1);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                const uint32_t q_lo = ((ptx::smem_u32(smem + Cf::kRingOff) + st * Cf::kTileBytes) >> 4) | lo;
+                const uint32_t q_lo = ((ptx::smem_u32(smem + Cf::kRingOff) + y * Cf::kTileBytes) >> 4) | lo;
                 const uint32_t idesc = umma::idesc_bf16_f32(128, slices - 2 * j >= 2 ? 128 : 64, 0);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * Cf::kBoxBytes + (kk & 3) * 32) >> 4;
-                    ptx::mma_ss_one(tmem + 128 * buf, desc_hi | (k_lo + off), desc_hi | (q_lo + off), idesc,
+                    ptx::mma_ss_one(tmem + 128 * y, desc_hi | (k_lo + off), desc_hi | (q_lo + off), idesc,
                                     kk > 0 ? 1u : 0u);
                 }
-                ptx::tc_commit_one(s_full + buf);
-                ptx::tc_commit_one(ring_empty + st);
-            }
-            if (!ok && lane == 0) {
-                atomicCAS(status, 0, 5);
-                *abort_flag = 1;
-            }
-        } else if (warp == 2) {
-            // ---------------------------------------------------------------- nlse
-            // the loads of a stage are issued two stages before they are stored
-            bool ok = true;
-            float a[2][4];
-            auto fetch = [&](int j, float (&r)[4]) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int s = it.s0 + 2 * j + (x >> 1);
-                    r[x] = INFINITY;
-                    if (s < it.s1) {
-                        const int i = it.row(s) + 32 * (x & 1) + lane;
-                        if (i <= it.i_hi)
-                            r[x] = lse[((int64_t)it.b * H + it.hk * (H / Hkv) + it.head(s)) * T + i];
-                    }
-                }
-            };
-            fetch(0, a[0]);
-            fetch(1, a[1]);
-            for (int j0 = 0; j0 < stages && ok; j0 += 2) {
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int j = j0 + y;
-                    if (j >= stages || !ok) break;
-                    const int st = j % kKwStats;
-                    if (j >= kKwStats)
-                        ok = __all_sync(0xffffffffu, ptx::mbar_wait(nl_free + st, ((j / kKwStats) - 1) & 1, wait_limit_ns,
-                                                                    abort_flag));
-                    if (!ok) break;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) sm_nl[128 * st + 32 * x + lane] = a[y][x] * -1.4426950408889634f;
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(nl_full + st);
-                    fetch(j + 2, a[y]);
-                }
+                ptx::tc_commit_one(s_full + y);
             }
             if (!ok && lane == 0) {
                 atomicCAS(status, 0, 5);
@@ -366,47 +315,58 @@ __global__ void __launch_bounds__(kKwThreads, 2)
             }
         } else {
             // ---------------------------------------------------------------- exponentials, sums
-            const int quarter = warp & 3, half = (warp - 3) >> 2;
-            const int row = 32 * quarter + lane, jk = it.j0 + row;
-            const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16) + 64 * half;
+            const int quarter = warp & 3, y = (warp - 2) >> 2;
+            const int jk = it.j0 + 32 * quarter + lane;
+            const uint32_t col = tmem + ((uint32_t)(32 * quarter) << 16) + 128 * y;
+            // a slice is full when every key of the tile is in the band of each of its rows
+            const int full_lo = it.j0 + 127, full_hi = min(it.j0 + W - 1, it.i_hi) - (kKwSlice - 1);
+            const int see = min(jk + W - 1, it.i_hi);  // this key is seen by queries jk .. see
+            int at = (it.s0 + 2 * y) % it.per_head;  // slice of its head, at the stage's first
             ptx::f32x2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
             bool ok = true;
-            for (int j = 0; j < stages; ++j) {
-                const int buf = j & 1, st = j % kKwStats;
-                ok = ptx::mbar_wait(s_full + buf, (j >> 1) & 1, wait_limit_ns, abort_flag) &&
-                     ptx::mbar_wait(nl_full + st, (j / kKwStats) & 1, wait_limit_ns, abort_flag);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+            for (int j = y; j < stages; j += 2) {
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full + y, (j >> 1) & 1, wait_limit_ns, abort_flag));
+                if (!ok) break;
                 ptx::tc_fence_after();
-                const int s = it.s0 + 2 * j + half;
-                const bool have = s < it.s1;  // uniform in the warp
-                const int i0 = have ? it.row(s) : 0;
-                // columns of this slice that see this thread's key
-                const int cmin = jk - i0, cmax = min((int)min((int64_t)jk + W - 1, (int64_t)it.i_hi) - i0, kKwSlice - 1);
-                const bool full = i0 >= it.j0 + 127 && (int64_t)i0 + 63 <= (int64_t)it.j0 + W - 1 && i0 + 63 <= it.i_hi;
-                const float* nl = sm_nl + 128 * st + 64 * half;
+                const int at1 = at + 1 < it.per_head ? at + 1 : 0;
+                const int i0 = it.i_lo + kKwSlice * at, i1 = it.i_lo + kKwSlice * at1;
+                const bool two = slices - 2 * j >= 2;
+                const bool full0 = i0 >= full_lo && i0 <= full_hi, full1 = i1 >= full_lo && i1 <= full_hi;
+                const float* nl = sm_nl + 128 * (j % kKwStats);
+                if (full0 && full1 && two) {
+                    // 16 columns at a time, the next ones on their way during the arithmetic
+                    uint32_t v[2][16];
+                    ptx::tmem_ld16(col, v[0]);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t v[32];
-                    if (have) {
-                        ptx::tmem_ld32(tl + 128 * buf + 32 * x, v);
+                    for (int x = 0; x < 8; ++x) {
+                        ptx::tmem_ld_wait();
+                        ptx::reg_fence(v[x & 1]);
+                        if (x < 7) {
+                            ptx::tmem_ld16(col + 16 * (x + 1), v[(x + 1) & 1]);
+                        } else {
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(s_read + y);
+                        }
+                        kw_sum16<false>(v[x & 1], nl + 16 * x, c2, 0, acc);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int x = 0; x < (two ? 8 : 4); ++x) {
+                        uint32_t v[16];
+                        ptx::tmem_ld16(col + 16 * x, v);
                         ptx::tmem_ld_wait();
                         ptx::reg_fence(v);
+                        const int c0 = (x < 4 ? i0 : i1) + 16 * (x & 3);  // the query of the first column
+                        const int lo = min(max(jk - c0, 0), 16), hi = min(max(see - c0 + 1, lo), 16);
+                        kw_sum16<true>(v, nl + 16 * x, c2, (1u << hi) - (1u << lo), acc);
                     }
-                    if (x == 1) {
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(s_read + buf);
-                    }
-                    if (have) {
-                        if (full) kw_sum32<false>(v, nl + 32 * x, c2, 0, 31, acc);
-                        else kw_sum32<true>(v, nl + 32 * x, c2, cmin - 32 * x, cmax - 32 * x, acc);
-                    }
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(s_read + y);
                 }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(nl_free + st);
+                at += 4;
+                while (at >= it.per_head) at -= it.per_head;
             }
             sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
             if (!ok) {
@@ -421,10 +381,8 @@ __global__ void __launch_bounds__(kKwThreads, 2)
         if (*abort_flag) {
             if (warp == 0 && lane == 0) {
                 ptx::mbar_wait(k_full, 0, kPPDrainLimitNs, nullptr);
-                for (uint32_t st = 0; st < (uint32_t)NS && st < loads; ++st) {
-                    const uint32_t t = st + ((loads - 1 - st) / NS) * NS;
-                    ptx::mbar_wait(ring_full + st, (t / NS) & 1, kPPDrainLimitNs, nullptr);
-                }
+                for (uint32_t y = 0; y < 2 && y < loads; ++y)
+                    ptx::mbar_wait(ring_full + y, ((loads - 1 - y) / 2) & 1, kPPDrainLimitNs, nullptr);
             }
             if (warp == 1) {
                 ptx::tc_commit_one(drain);
@@ -439,8 +397,8 @@ __global__ void __launch_bounds__(kKwThreads, 2)
         }
     }
 
-    // the sums of the two slices' threads, then of the cluster's CTAs, in that order
-    if (warp >= 3) sm_red[128 * ((warp - 3) >> 2) + 32 * (warp & 3) + lane] = sum;
+    // the sums of the two warpgroups, then of the cluster's CTAs, in that order
+    if (warp >= 2) sm_red[128 * ((warp - 2) >> 2) + 32 * (warp & 3) + lane] = sum;
     if (C > 1) {
         asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     } else {
@@ -449,12 +407,12 @@ __global__ void __launch_bounds__(kKwThreads, 2)
     if (rank == 0 && tid < 128) {
         float w = sm_red[tid] + sm_red[128 + tid];
         for (int r = 1; r < C; ++r) {
-            float x, y;
-            uint32_t at;
-            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(sm_red + tid)), "r"(r));
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at));
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y) : "r"(at + 512));
-            w += x + y;
+            float x, z;
+            uint32_t from;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(ptx::smem_u32(sm_red + tid)), "r"(r));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(from));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(z) : "r"(from + 512));
+            w += x + z;
         }
         const int j = it.j0 + tid;
         // a key past the stream's end may have met anything in its row
