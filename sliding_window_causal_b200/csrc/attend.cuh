@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
 __device__ __forceinline__ uint32_t word(const uint4& u, int w) { return w == 0 ? u.x : w == 1 ? u.y : w == 2 ? u.z : u.w; }
 
 // PREFIX: the keys are the shared prefix and the queries are all streams' (row r of key head hk
-// is stream r / G, head hk G + r % G); else the keys are stream b's slots 0 .. min(pos+1, S)-1.
+// is stream r / G, head hk G + r % G; up to kAttendQueries rows, more go to prefix_kernel); else the keys are stream b's slots 0 .. min(pos+1, S)-1.
 template <int D, bool PREFIX, bool SCORES>
 __global__ void __launch_bounds__(kAttendWarps * 32) attend_kernel(const AttendArgs a) {
     constexpr int KL = D / 32;  // 16-byte pieces of a key row per lane

@@ -16,6 +16,7 @@
 #include "attend.cuh"
 #include "cache.cuh"
 #include "keyweights.cuh"
+#include "prefix.cuh"
 #include "swa.h"
 
 namespace {
@@ -97,8 +98,9 @@ void launch_after(dim3 grid, unsigned block, size_t smem, cudaStream_t s, void (
     cudaLaunchKernelEx(&c, kernel, args...);
 }
 
-// Let `kernel` use `bytes` of dynamic shared memory on the current device (once a device).
-int allow_smem(const void* kernel, int bytes) {
+// Let `kernel` use `bytes` of dynamic shared memory on the current device, and check that it was
+// compiled with `regs` registers a thread if that is given (once a device).
+int allow_smem(const void* kernel, int bytes, int regs = 0) {
     static std::mutex mu;
     static std::set<std::pair<int, const void*>> done;
     int dev;
@@ -108,6 +110,11 @@ int allow_smem(const void* kernel, int bytes) {
     if (done.count({dev, kernel})) return SWA_OK;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return fail(SWA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, kernel);
+    if (e != cudaSuccess) return fail(SWA_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
+    if (regs > 0 && at.numRegs != regs)
+        return fail(SWA_ERR_CUDA, "a kernel was compiled with %d registers a thread, %d expected", at.numRegs, regs);
     done.insert({dev, kernel});
     return SWA_OK;
 }
@@ -147,7 +154,8 @@ int launch_key_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const f
 // call always agree.
 struct Plan {
     int ns, chunk;    // the streams' slots
-    int np, pchunk;   // the prefix
+    int np, pchunk;   // the prefix: partial states a row; keys a split takes (key tiles with tc)
+    bool tc, pair;    // the prefix on the tensor cores; two row tiles a CTA
     int64_t NS;
     int64_t off_o, off_scores, bytes;  // workspace: (m, l), o, scores
 };
@@ -161,13 +169,40 @@ void split(int64_t units, int64_t keys, int* n, int* chunk) {
     *n = (int)((keys + c - 1) / c);
 }
 
+// The prefix on the tensor cores when more rows share its keys than one CTA of attend_kernel
+// serves.
+constexpr int64_t kPrefixTcRows = swa::kAttendQueries + 1;
+
+// Key tiles that a CTA of prefix_kernel takes, of `tiles`, when `groups` CTAs take them all: the
+// fewest rounds of 148 CTAs (one fits an SM) by the length of a round, where the start and end
+// of a CTA count as 3 tiles.
+int64_t prefix_chunk(int64_t groups, int64_t tiles) {
+    int64_t best = tiles, cost = INT64_MAX;
+    for (int64_t ns = 1; ns <= tiles && ns <= 148; ++ns) {
+        const int64_t chunk = (tiles + ns - 1) / ns, rounds = (groups * ((tiles + chunk - 1) / chunk) + 147) / 148;
+        if (rounds * (chunk + 3) < cost) {
+            cost = rounds * (chunk + 3);
+            best = chunk;
+        }
+    }
+    return best;
+}
+
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
 Plan plan(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D, bool scores) {
     Plan p = {};
     const int64_t G = H / Hkv, Q = swa::kAttendQueries;
     split(B * Hkv * ((G + Q - 1) / Q), S, &p.ns, &p.chunk);
-    if (P > 0) split(Hkv * ((B * G + Q - 1) / Q), P, &p.np, &p.pchunk);
+    p.tc = P > 0 && B * G >= kPrefixTcRows;
+    p.pair = B * G > 128;
+    if (p.tc) {
+        const int64_t tiles = (P + 127) / 128;
+        p.pchunk = (int)prefix_chunk(Hkv * (p.pair ? (B * G + 255) / 256 : 1), tiles);
+        p.np = (int)((tiles + p.pchunk - 1) / p.pchunk) * (p.pair ? 1 : 2);
+    } else if (P > 0) {
+        split(Hkv, P, &p.np, &p.pchunk);
+    }
     p.NS = p.ns + p.np;
     p.off_o = round256(B * H * p.NS * 8);
     p.off_scores = p.off_o + round256(B * H * p.NS * D * 4);
@@ -187,15 +222,32 @@ int check_decode_sizes(const char* fn, int64_t B, int64_t H, int64_t Hkv, int64_
     return SWA_OK;
 }
 
+template <int D, bool PAIR>
+int launch_prefix(const Plan& pl, const swa::AttendArgs& pre, cudaStream_t s) {
+    using Cf = swa::PrefixCfg<D, PAIR>;
+    auto* kernel = swa::prefix_kernel<D, PAIR>;
+    // its register split assumes this many registers a thread at launch
+    if (int rc = allow_smem(reinterpret_cast<const void*>(kernel), Cf::kSmemBytes, swa::kPPLaunchRegs)) return rc;
+    CUtensorMap tm_k, tm_v;
+    const int64_t P = pre.S, ks[3] = {D, pre.k_head, pre.k_row}, vs[3] = {D, pre.v_head, pre.v_row};
+    if (int rc = swa_internal::tensor_map(&tm_k, pre.k, 1, pre.Hkv, P, D, ks, 128)) return rc;
+    if (int rc = swa_internal::tensor_map(&tm_v, pre.v, 1, pre.Hkv, P, D, vs, 128)) return rc;
+    const int64_t rows = (int64_t)pre.B * pre.G, groups = PAIR ? (rows + 255) / 256 : 1;
+    const dim3 grid((unsigned)(pre.Hkv * groups), (unsigned)(pl.np / (PAIR ? 1 : 2)));
+    kernel<<<grid, swa::kPrefixThreads, Cf::kSmemBytes, s>>>(tm_k, tm_v, pre, swa_internal::wait_limit_ns());
+    return launched("prefix");
+}
+
 template <int D>
-void launch_decode(const Plan& pl, const swa::AttendArgs& ring, const swa::AttendArgs& pre, __nv_bfloat16* out,
-                   float* weights, cudaStream_t s) {
+int launch_decode(const Plan& pl, const swa::AttendArgs& ring, const swa::AttendArgs& pre, __nv_bfloat16* out,
+                  float* weights, cudaStream_t s) {
     const int Q = swa::kAttendQueries;
     const int64_t units = (int64_t)ring.B * ring.Hkv;
     const unsigned threads = swa::kAttendWarps * 32;
-    if (pl.np > 0) {
-        const dim3 grid((unsigned)((int64_t)ring.Hkv * (((int64_t)ring.B * ring.G + Q - 1) / Q)), (unsigned)pl.np);
-        swa::attend_kernel<D, true, false><<<grid, threads, 0, s>>>(pre);
+    if (pl.tc) {
+        if (int rc = pl.pair ? launch_prefix<D, true>(pl, pre, s) : launch_prefix<D, false>(pl, pre, s)) return rc;
+    } else if (pl.np > 0) {
+        swa::attend_kernel<D, true, false><<<dim3((unsigned)ring.Hkv, (unsigned)pl.np), threads, 0, s>>>(pre);
     }
     const dim3 grid((unsigned)(units * ((ring.G + Q - 1) / Q)), (unsigned)pl.ns);
     if (weights) swa::attend_kernel<D, false, true><<<grid, threads, 0, s>>>(ring);
@@ -204,6 +256,7 @@ void launch_decode(const Plan& pl, const swa::AttendArgs& ring, const swa::Atten
     const int64_t blocks = (int64_t)ring.B * ring.H + units * slot_blocks;
     launch_after(dim3((unsigned)blocks), swa::kFinishThreads, (size_t)ring.G * 4, s, swa::finish_kernel<D>, ring, out,
                  weights, slot_blocks);
+    return SWA_OK;
 }
 
 int decode(const char* fn, const void* q, const void* k, const void* v, const int64_t* pos, const void* kp, const void* vp,
@@ -231,7 +284,7 @@ int decode(const char* fn, const void* q, const void* k, const void* v, const in
     }
     const int64_t G = H / Hkv;
     const int64_t blocks = B * H + (scores ? B * Hkv * ((S + swa::kFinishSlots - 1) / swa::kFinishSlots) : 0);
-    if (blocks > INT32_MAX || pl.ns > 65535 || pl.np > 65535) return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    if (blocks > INT32_MAX || pl.ns > 65535) return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     int *status, num_sms;
     if (int rc = swa_internal::device_info(&status, &num_sms)) return rc;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -268,8 +321,7 @@ int decode(const char* fn, const void* q, const void* k, const void* v, const in
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto* ob = static_cast<__nv_bfloat16*>(out);
     float* w = scores ? weights : nullptr;
-    if (D == 128) launch_decode<128>(pl, a, pre, ob, w, s);
-    else launch_decode<64>(pl, a, pre, ob, w, s);
+    if (int rc = D == 128 ? launch_decode<128>(pl, a, pre, ob, w, s) : launch_decode<64>(pl, a, pre, ob, w, s)) return rc;
     if (int rc = launched(fn)) return rc;
     return success();
 }

@@ -262,9 +262,13 @@ def test_cache_append_orders_weights_and_reports_full_heads():
 # -------------------------------------------------------------------------- decode
 
 
-def check_decode(q, kc, vc, pos, kp=None, vp=None, scale=None, wc=None, p_step=2.0 ** -16, **kw):
+def check_decode(q, kc, vc, pos, kp=None, vp=None, scale=None, wc=None, **kw):
     """One call through the package, with or without weights, against float64."""
     S = kc.shape[2]
+    # Softmax weights are carried as two bf16 parts (2 ** -16 of a weight), except over a prefix
+    # that more than 128 query rows share: there as one, each weight off by half a step of bf16,
+    # 2 ** -8 of itself, so an output sum p (1 + e) v by at most 2 ** -8 of sum p |v|.
+    p_step = ref.UBF if kp is not None and q.shape[0] * (q.shape[1] // kc.shape[1]) > 128 else 2.0 ** -16
     want, spread, gain, ez = ref.decode(q, kc, vc, pos, kp, vp, scale)
     keys = S + (0 if kp is None else kp.shape[1])
     if wc is None:
