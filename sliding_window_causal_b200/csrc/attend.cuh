@@ -3,15 +3,16 @@
 //
 // The softmax of a row is taken in splits of its keys, each an online softmax state
 //   m = max_j z_j,  l = sum_j 2^(z_j - m),  o = sum_j 2^(z_j - m) v_j,   z = scale log2(e) q.k,
-// and joined by finish_kernel: m* = max m, out = sum 2^(m - m*) o / sum 2^(m - m*) l.
+// and joined: m* = max m, out = sum 2^(m - m*) o / sum 2^(m - m*) l.
 //
-// attend_kernel: CTA = (key head, 8 queries, split of the keys). The keys are read once for the
-// 8 queries that share them, so the kernel is bound by HBM: 4 D bytes a slot against 32 D
-// multiply-adds. The products go through m16n8k16 with the keys as the 16 rows (S^T = K Q^T
-// and O^T = V^T P^T), which spends no tile rows on missing queries. Every fragment comes
-// straight from 16-byte loads: the order of the head dimension inside a product is free as
-// long as K and Q agree (a lane's 16 bytes are two k-steps), and in O^T it is the order of
-// the output rows. P crosses from accumulator to operand layout by an 8x8 transpose inside
+// A CTA takes some keys for up to 8 queries that share them, so HBM is the bound: 4 D bytes a key
+// against 32 D multiply-adds. stream_kernel: a cluster of CTAs finishes a (stream, key head) by
+// itself. attend_kernel: any number of splits, when a cluster is too few CTAs for the keys or
+// there are more than 8 queries, joined by finish_kernel. The products go through m16n8k16 with
+// the keys as the 16 rows (S^T = K Q^T and O^T = V^T P^T), which spends no tile rows on missing
+// queries. Every fragment comes straight from 16-byte loads: the order of the head dimension
+// inside a product is free as long as K and Q agree (a lane's 16 bytes are two k-steps), and in
+// O^T it is the order of the output rows. P crosses from accumulator to operand layout by an 8x8 transpose inside
 // the warp. P is carried as two bf16 parts (hi + lo, 16 bits of weight), so that the output
 // is rounded once: the products are far from bounding the kernel. m, l, o are fp32; o and l
 // are rescaled only when a score passes m by more than 2^8.
@@ -35,7 +36,7 @@ struct AttendArgs {
     const __nv_bfloat16* q;    // [B, H, D]
     const __nv_bfloat16* k;    // ring or cache [B, Hkv, S, D]; prefix: (h, t) strides
     const __nv_bfloat16* v;
-    const int64_t* pos;        // [B]; not read for the prefix
+    const int64_t* pos;        // [B]; not read by prefix_kernel
     float2* ml;                // [B*H][NS] (m, l)
     float* o;                  // [B*H][NS][D]
     float* scores;             // [B*Hkv][G][S] z of every slot, or null
@@ -58,188 +59,366 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+// The slots that the query at position P sees: none, and a report, if it is negative.
+__device__ __forceinline__ int attend_slots(int64_t P, int S, int* status, bool report) {
+    if (P >= 0) return (int)(P + 1 < (int64_t)S ? P + 1 : (int64_t)S);
+    if (report) atomicCAS(status, 0, kStatusInvalid);
+    return 0;
+}
 __device__ __forceinline__ uint32_t word(const uint4& u, int w) { return w == 0 ? u.x : w == 1 ? u.y : w == 2 ? u.z : u.w; }
 
-// PREFIX: the keys are the shared prefix and the queries are all streams' (row r of key head hk
-// is stream r / G, head hk G + r % G; up to kAttendQueries rows, more go to prefix_kernel); else the keys are stream b's slots 0 .. min(pos+1, S)-1.
-template <int D, bool PREFIX, bool SCORES>
-__global__ void __launch_bounds__(kAttendWarps * 32) attend_kernel(const AttendArgs a) {
-    constexpr int KL = D / 32;  // 16-byte pieces of a key row per lane
-    constexpr int VL = D / 64;  // 16-byte pieces of a value row per lane
-    constexpr int MT = D / 16;  // 16-row tiles of O^T
-    __shared__ float sm_m[kAttendWarps][kAttendQueries], sm_l[kAttendWarps][kAttendQueries];
-    __shared__ float sm_o[kAttendWarps][kAttendQueries][D + 8];
+// The online softmax of 8 queries over some keys, as one warp of a CTA holds it: queries 2t and
+// 2t+1 of lane (g, t), o in the layout of the accumulators of O^T.
+template <int D>
+struct AttendState {
+    static constexpr int KL = D / 32;  // 16-byte pieces of a key row per lane
+    static constexpr int VL = D / 64;  // 16-byte pieces of a value row per lane
+    static constexpr int MT = D / 16;  // 16-row tiles of O^T
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float o[MT][4];
+    uint32_t qf[KL][4];  // B fragments of Q^T: query g
 
+    // qr: query g's row, or null
+    __device__ __forceinline__ void start(const __nv_bfloat16* qr, int t) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KL; ++i) {
+            const uint4 u = qr ? *reinterpret_cast<const uint4*>(qr + 32 * i + 8 * t) : make_uint4(0, 0, 0, 0);
+            qf[i][0] = u.x; qf[i][1] = u.y; qf[i][2] = u.z; qf[i][3] = u.w;
+        }
+    }
+
+    // Keys r0 .. r1-1 of k, v (row strides k_row, v_row); the CTA's warps take 16 each in turn.
+    // put(query, key, z) gets every score.
+    template <typename Put>
+    __device__ __forceinline__ void keys(const __nv_bfloat16* k, const __nv_bfloat16* v, int64_t k_row, int64_t v_row,
+                                         int r0, int r1, float scale_log2, int warp, int g, int t, Put put) {
+        const __nv_bfloat16* kb = k + 8 * t;
+        const __nv_bfloat16* vb = v + 8 * g;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        for (int base = r0 + 16 * warp; base < r1; base += kAttendStep) {
+            uint4 kr[2][KL], vr[4][VL];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int slot = base + g + 8 * x;
+#pragma unroll
+                for (int i = 0; i < KL; ++i) kr[x][i] = slot < r1 ? ld_stream_16(kb + slot * k_row + 32 * i) : zero;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int slot = base + 2 * t + (x & 1) + 8 * (x >> 1);
+#pragma unroll
+                for (int i = 0; i < VL; ++i) vr[x][i] = slot < r1 ? ld_stream_16(vb + slot * v_row + 64 * i) : zero;
+            }
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < KL; ++i) {
+                mma_bf16(c, kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y, qf[i][0], qf[i][1]);
+                mma_bf16(c, kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, qf[i][2], qf[i][3]);
+            }
+            const bool v0 = base + g < r1, v1 = base + g + 8 < r1;
+            const float z0 = v0 ? c[0] * scale_log2 : -INFINITY, z1 = v0 ? c[1] * scale_log2 : -INFINITY;
+            const float z2 = v1 ? c[2] * scale_log2 : -INFINITY, z3 = v1 ? c[3] * scale_log2 : -INFINITY;
+            if (v0) {
+                put(2 * t, base + g, z0);
+                put(2 * t + 1, base + g, z1);
+            }
+            if (v1) {
+                put(2 * t, base + g + 8, z2);
+                put(2 * t + 1, base + g + 8, z3);
+            }
+            float t0 = fmaxf(z0, z2), t1 = fmaxf(z1, z3);
+            if (__any_sync(0xffffffffu, t0 > m0 + kAttendRescale || t1 > m1 + kAttendRescale)) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+                    t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
+                    t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
+                }
+                const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+                const float f0 = m0 == -INFINITY ? 0.f : ptx::ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - n1);
+                m0 = n0;
+                m1 = n1;
+                l0 *= f0;
+                l1 *= f1;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    o[i][0] *= f0;
+                    o[i][1] *= f1;
+                    o[i][2] *= f0;
+                    o[i][3] *= f1;
+                }
+            }
+            const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+            const float p0 = ptx::ex2(z0 - u0), p1 = ptx::ex2(z1 - u1), p2 = ptx::ex2(z2 - u0), p3 = ptx::ex2(z3 - u1);
+            l0 += p0 + p2;
+            l1 += p1 + p3;
+            const uint32_t h01 = ptx::pack_bf16x2(p0, p1), h23 = ptx::pack_bf16x2(p2, p3);
+            const uint32_t e01 = ptx::pack_bf16x2(p0 - ptx::bf16lo_f32(h01), p1 - ptx::bf16hi_f32(h01));
+            const uint32_t e23 = ptx::pack_bf16x2(p2 - ptx::bf16lo_f32(h23), p3 - ptx::bf16hi_f32(h23));
+            const uint32_t bh0 = transpose_8x8(h01), bh1 = transpose_8x8(h23);
+            const uint32_t bl0 = transpose_8x8(e01), bl1 = transpose_8x8(e23);
+#pragma unroll
+            for (int i = 0; i < VL; ++i)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t x0 = word(vr[0][i], w), x1 = word(vr[1][i], w), x2 = word(vr[2][i], w), x3 = word(vr[3][i], w);
+                    const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
+                    const uint32_t a2 = __byte_perm(x2, x3, 0x5410), a3 = __byte_perm(x2, x3, 0x7632);
+                    mma_bf16(o[4 * i + w], a0, a1, a2, a3, bh0, bh1);
+                    mma_bf16(o[4 * i + w], a0, a1, a2, a3, bl0, bl1);
+                }
+        }
+    }
+};
+
+// The states of a CTA's warps, joined: done(query, d, M, L, A) for every 4 columns d of the
+// first nq queries, once each. done runs after every read of sm_m and sm_l, and after the reads
+// of its own columns of o.
+template <int D>
+struct AttendJoin {
+    float m[kAttendWarps][kAttendQueries], l[kAttendWarps][kAttendQueries];
+    float o[kAttendWarps][kAttendQueries][D + 8];
+
+    template <typename Done>
+    __device__ __forceinline__ void run(AttendState<D>& st, int nq, int tid, Done done) {
+        const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+            st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, x);
+            st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, x);
+        }
+        if (g == 0) {
+            m[warp][2 * t] = st.m0;
+            m[warp][2 * t + 1] = st.m1;
+            l[warp][2 * t] = st.l0;
+            l[warp][2 * t + 1] = st.l1;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int d = 64 * i + 8 * g + 2 * w;
+                *reinterpret_cast<float2*>(&o[warp][2 * t][d]) = make_float2(st.o[4 * i + w][0], st.o[4 * i + w][2]);
+                *reinterpret_cast<float2*>(&o[warp][2 * t + 1][d]) = make_float2(st.o[4 * i + w][1], st.o[4 * i + w][3]);
+            }
+        __syncthreads();
+        for (int x = tid; x < nq * (D / 4); x += kAttendWarps * 32) {
+            const int i = x / (D / 4), d = (x % (D / 4)) * 4;
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kAttendWarps; ++w) M = fmaxf(M, m[w][i]);
+            float L = 0.f;
+            float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kAttendWarps; ++w) {
+                // a warp without a key has l = 0 and o = 0
+                const float f = m[w][i] == -INFINITY ? 0.f : ptx::ex2(m[w][i] - M);
+                L = fmaf(l[w][i], f, L);
+                const float4 v = *reinterpret_cast<const float4*>(&o[w][i][d]);
+                A.x = fmaf(v.x, f, A.x);
+                A.y = fmaf(v.y, f, A.y);
+                A.z = fmaf(v.z, f, A.z);
+                A.w = fmaf(v.w, f, A.w);
+            }
+            done(i, d, M, L, A);
+        }
+    }
+};
+
+// ------------------------------------------------------------------ splits of any number
+// CTA = (stream, key head, 8 of its queries, split of the slots 0 .. min(pos+1, S)-1).
+template <int D, bool SCORES>
+__global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) attend_kernel(const AttendArgs a) {
+    __shared__ AttendJoin<D> join;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const int s = blockIdx.y;
-    const int n_rows = PREFIX ? a.B * a.G : a.G;  // queries that share these keys
-    const int qtiles = (n_rows + kAttendQueries - 1) / kAttendQueries;
-    const int64_t unit = blockIdx.x / qtiles;  // hk, or b * Hkv + hk
+    const int qtiles = (a.G + kAttendQueries - 1) / kAttendQueries;
+    const int64_t unit = blockIdx.x / qtiles, b = unit / a.Hkv;
     const int q0 = (int)(blockIdx.x % qtiles) * kAttendQueries;
-    const int nq = min(kAttendQueries, n_rows - q0);
-    const int hk = PREFIX ? (int)unit : (int)(unit % a.Hkv);
-    const int64_t b0 = PREFIX ? 0 : unit / a.Hkv;
-    auto row_of = [&](int i) -> int64_t {  // query i of this CTA
-        const int r = q0 + i;
-        return PREFIX ? (int64_t)(r / a.G) * a.H + hk * a.G + r % a.G : b0 * a.H + hk * a.G + r;
-    };
-
-    int n = a.S;
-    if (!PREFIX) {
-        const int64_t P = a.pos[b0];
-        if (P < 0) {
-            if (tid == 0 && s == 0) atomicCAS(a.status, 0, kStatusInvalid);
-            n = 0;
-        } else {
-            n = (int)(P + 1 < (int64_t)a.S ? P + 1 : (int64_t)a.S);
-        }
-    }
+    const int nq = min(kAttendQueries, a.G - q0);
+    const int64_t row0 = b * a.H + (unit - b * a.Hkv) * a.G + q0;
+    const int n = attend_slots(a.pos[b], a.S, a.status, tid == 0 && s == 0);
     const int r0 = s * a.chunk;
     const int r1 = min(r0 + a.chunk, n);
     if (r0 >= r1) {  // nothing of this split is valid
-        if (tid < nq) a.ml[row_of(tid) * a.NS + a.split0 + s] = make_float2(-INFINITY, 0.f);
+        if (tid < nq) a.ml[(row0 + tid) * a.NS + a.split0 + s] = make_float2(-INFINITY, 0.f);
         return;
     }
-
-    uint32_t qf[KL][4];  // B fragments of Q^T: query g
-    if (g < nq) {
-        const __nv_bfloat16* qr = a.q + row_of(g) * D;
-#pragma unroll
-        for (int i = 0; i < KL; ++i) {
-            const uint4 u = *reinterpret_cast<const uint4*>(qr + 32 * i + 8 * t);
-            qf[i][0] = u.x; qf[i][1] = u.y; qf[i][2] = u.z; qf[i][3] = u.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < KL; ++i) qf[i][0] = qf[i][1] = qf[i][2] = qf[i][3] = 0u;
-    }
-    const __nv_bfloat16* kb = a.k + unit * a.k_head + 8 * t;
-    const __nv_bfloat16* vb = a.v + unit * a.v_head + 8 * g;
+    AttendState<D> st;
+    st.start(g < nq ? a.q + (row0 + g) * D : nullptr, t);
     float* zrow = SCORES ? a.scores + (unit * a.G + q0) * a.S : nullptr;
-
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // queries 2t, 2t+1
-    float o[MT][4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int base = r0 + 16 * warp; base < r1; base += kAttendStep) {
-        uint4 kr[2][KL], vr[4][VL];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int slot = base + g + 8 * x;
-#pragma unroll
-            for (int i = 0; i < KL; ++i) kr[x][i] = slot < r1 ? ld_stream_16(kb + slot * a.k_row + 32 * i) : zero;
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int slot = base + 2 * t + (x & 1) + 8 * (x >> 1);
-#pragma unroll
-            for (int i = 0; i < VL; ++i) vr[x][i] = slot < r1 ? ld_stream_16(vb + slot * a.v_row + 64 * i) : zero;
-        }
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < KL; ++i) {
-            mma_bf16(c, kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y, qf[i][0], qf[i][1]);
-            mma_bf16(c, kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, qf[i][2], qf[i][3]);
-        }
-        const bool v0 = base + g < r1, v1 = base + g + 8 < r1;
-        const float z0 = v0 ? c[0] * a.scale_log2 : -INFINITY, z1 = v0 ? c[1] * a.scale_log2 : -INFINITY;
-        const float z2 = v1 ? c[2] * a.scale_log2 : -INFINITY, z3 = v1 ? c[3] * a.scale_log2 : -INFINITY;
-        if (SCORES) {
-            if (2 * t < nq) {
-                if (v0) zrow[(int64_t)(2 * t) * a.S + base + g] = z0;
-                if (v1) zrow[(int64_t)(2 * t) * a.S + base + g + 8] = z2;
-            }
-            if (2 * t + 1 < nq) {
-                if (v0) zrow[(int64_t)(2 * t + 1) * a.S + base + g] = z1;
-                if (v1) zrow[(int64_t)(2 * t + 1) * a.S + base + g + 8] = z3;
-            }
-        }
-        float t0 = fmaxf(z0, z2), t1 = fmaxf(z1, z3);
-        if (__any_sync(0xffffffffu, t0 > m0 + kAttendRescale || t1 > m1 + kAttendRescale)) {
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) {
-                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
-                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
-            }
-            const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
-            const float f0 = m0 == -INFINITY ? 0.f : ptx::ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - n1);
-            m0 = n0;
-            m1 = n1;
-            l0 *= f0;
-            l1 *= f1;
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                o[i][0] *= f0;
-                o[i][1] *= f1;
-                o[i][2] *= f0;
-                o[i][3] *= f1;
-            }
-        }
-        const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
-        const float p0 = ptx::ex2(z0 - u0), p1 = ptx::ex2(z1 - u1), p2 = ptx::ex2(z2 - u0), p3 = ptx::ex2(z3 - u1);
-        l0 += p0 + p2;
-        l1 += p1 + p3;
-        const uint32_t h01 = ptx::pack_bf16x2(p0, p1), h23 = ptx::pack_bf16x2(p2, p3);
-        const uint32_t e01 = ptx::pack_bf16x2(p0 - ptx::bf16lo_f32(h01), p1 - ptx::bf16hi_f32(h01));
-        const uint32_t e23 = ptx::pack_bf16x2(p2 - ptx::bf16lo_f32(h23), p3 - ptx::bf16hi_f32(h23));
-        const uint32_t bh0 = transpose_8x8(h01), bh1 = transpose_8x8(h23);
-        const uint32_t bl0 = transpose_8x8(e01), bl1 = transpose_8x8(e23);
-#pragma unroll
-        for (int i = 0; i < VL; ++i)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint32_t x0 = word(vr[0][i], w), x1 = word(vr[1][i], w), x2 = word(vr[2][i], w), x3 = word(vr[3][i], w);
-                const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
-                const uint32_t a2 = __byte_perm(x2, x3, 0x5410), a3 = __byte_perm(x2, x3, 0x7632);
-                mma_bf16(o[4 * i + w], a0, a1, a2, a3, bh0, bh1);
-                mma_bf16(o[4 * i + w], a0, a1, a2, a3, bl0, bl1);
-            }
-    }
-#pragma unroll
-    for (int x = 4; x < 32; x <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-    }
-    if (g == 0) {
-        sm_m[warp][2 * t] = m0;
-        sm_m[warp][2 * t + 1] = m1;
-        sm_l[warp][2 * t] = l0;
-        sm_l[warp][2 * t + 1] = l1;
-    }
-#pragma unroll
-    for (int i = 0; i < VL; ++i)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const int d = 64 * i + 8 * g + 2 * w;
-            *reinterpret_cast<float2*>(&sm_o[warp][2 * t][d]) = make_float2(o[4 * i + w][0], o[4 * i + w][2]);
-            *reinterpret_cast<float2*>(&sm_o[warp][2 * t + 1][d]) = make_float2(o[4 * i + w][1], o[4 * i + w][3]);
-        }
-    __syncthreads();
-    for (int x = tid; x < nq * (D / 4); x += kAttendWarps * 32) {
-        const int i = x / (D / 4), d = (x % (D / 4)) * 4;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kAttendWarps; ++w) M = fmaxf(M, sm_m[w][i]);
-        float L = 0.f;
-        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kAttendWarps; ++w) {
-            // a warp without a slot has l = 0 and o = 0
-            const float f = sm_m[w][i] == -INFINITY ? 0.f : ptx::ex2(sm_m[w][i] - M);
-            L = fmaf(sm_l[w][i], f, L);
-            const float4 v = *reinterpret_cast<const float4*>(&sm_o[w][i][d]);
-            A.x = fmaf(v.x, f, A.x);
-            A.y = fmaf(v.y, f, A.y);
-            A.z = fmaf(v.z, f, A.z);
-            A.w = fmaf(v.w, f, A.w);
-        }
-        const int64_t at = row_of(i) * a.NS + a.split0 + s;
+    st.keys(a.k + unit * a.k_head, a.v + unit * a.v_head, a.k_row, a.v_row, r0, r1, a.scale_log2, warp, g, t,
+            [&](int i, int slot, float z) {
+                if (SCORES && i < nq) zrow[(int64_t)i * a.S + slot] = z;
+            });
+    join.run(st, nq, tid, [&](int i, int d, float M, float L, const float4& A) {
+        const int64_t at = (row0 + i) * a.NS + a.split0 + s;
         *reinterpret_cast<float4*>(a.o + at * D + d) = A;
         if (d == 0) a.ml[at] = make_float2(M, L);
+    });
+}
+
+// ------------------------------------------------------------------ one cluster per key head
+// stream_kernel: a cluster of C CTAs takes all keys of one (stream, key head): the first P0 keys
+// of the prefix, when it is short enough for every stream to read it by itself, and the slots.
+// Its CTAs join their states through distributed shared memory, together with the np partial
+// states that a kernel before it has left for the rest of the prefix, write the output rows and,
+// SCORES, add the attention weights from the scores they kept in shared memory: no workspace
+// but the prefix's, one launch, no traffic beyond the inputs and outputs. G <= 8.
+struct StreamArgs {
+    AttendArgs a;                 // slots; ml, o, NS: the np partial states of a row
+    const __nv_bfloat16* pk;      // the prefix: (h, t) strides
+    const __nv_bfloat16* pv;
+    int64_t pk_head, pk_row, pv_head, pv_row;
+    int P0, pchunk;               // prefix keys read here; keys of a CTA
+    int C;
+    __nv_bfloat16* out;
+    float* weights;
+};
+
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(ptx::smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float cluster_ld(uint32_t at) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at));
+    return x;
+}
+__device__ __forceinline__ void cluster_ld_vec(uint32_t at, float (&v)[4]) {
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(at));
+}
+__device__ __forceinline__ void cluster_ld_vec(uint32_t at, float (&v)[2]) {
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(at));
+}
+__device__ __forceinline__ void ldcg_vec(const float* p, float (&v)[4]) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+}
+__device__ __forceinline__ void ldcg_vec(const float* p, float (&v)[2]) {
+    const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+    v[0] = x.x; v[1] = x.y;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
+template <int D, bool SCORES>
+__global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_kernel(const StreamArgs sa) {
+    const AttendArgs& a = sa.a;
+    __shared__ AttendJoin<D> join;
+    __shared__ float sm_m[kAttendQueries], sm_l[kAttendQueries], sm_lse[kAttendQueries];
+    extern __shared__ float sm_z[];  // [G][chunk]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int C = sa.C, rank = (int)(blockIdx.x % C);
+    const int64_t unit = blockIdx.x / C, b = unit / a.Hkv;
+    const int hk = (int)(unit - b * a.Hkv), nq = a.G;
+    const int64_t row0 = b * a.H + hk * a.G;
+    const int64_t pos = a.pos[b];
+    const int n = attend_slots(pos, a.S, a.status, tid == 0 && rank == 0);
+    const int r0 = min(rank * a.chunk, n), r1 = min(r0 + a.chunk, n);
+
+    AttendState<D> st;
+    st.start(g < nq ? a.q + (row0 + g) * D : nullptr, t);
+    if (sa.P0 > 0) {
+        const int p0 = min(rank * sa.pchunk, sa.P0), p1 = min(p0 + sa.pchunk, sa.P0);
+        st.keys(sa.pk + hk * sa.pk_head, sa.pv + hk * sa.pv_head, sa.pk_row, sa.pv_row, p0, p1, a.scale_log2, warp, g, t,
+                [](int, int, float) {});
     }
+    st.keys(a.k + unit * a.k_head, a.v + unit * a.v_head, a.k_row, a.v_row, r0, r1, a.scale_log2, warp, g, t,
+            [&](int i, int slot, float z) {
+                if (SCORES && i < nq) sm_z[i * a.chunk + slot - r0] = z;
+            });
+    join.run(st, nq, tid, [&](int i, int d, float M, float L, const float4& A) {
+        *reinterpret_cast<float4*>(&join.o[0][i][d]) = A;
+        if (d == 0) {
+            sm_m[i] = M;
+            sm_l[i] = L;
+        }
+    });
+    if (C > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    ptx::grid_dependency_wait();  // the prefix's partial states
+    for (int i = warp; i < nq; i += kAttendWarps) {  // a warp joins a row
+        const int64_t row = row0 + i;
+        const float2* ml = a.ml + row * a.NS;
+        float cm = -INFINITY, cl = 0.f;  // lane: the state of CTA `lane`
+        if (lane < C) {
+            cm = cluster_ld(cluster_addr(&sm_m[i], lane));
+            cl = cluster_ld(cluster_addr(&sm_l[i], lane));
+        }
+        // the prefix's: of a lane, state `lane` of every 32 (the first 32 stay in registers)
+        const float2 e0 = lane < a.NS ? __ldcg(ml + lane) : make_float2(-INFINITY, 0.f);
+        float M = fmaxf(cm, e0.x);
+        for (int s = 32 + lane; s < a.NS; s += 32) M = fmaxf(M, __ldcg(ml + s).x);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+        const float cf = cm == -INFINITY ? 0.f : ptx::ex2(cm - M), f0 = e0.x == -INFINITY ? 0.f : ptx::ex2(e0.x - M);
+        float L = fmaf(cl, cf, e0.y * f0);
+        for (int s = 32 + lane; s < a.NS; s += 32) {
+            const float2 e = __ldcg(ml + s);
+            if (e.x != -INFINITY) L = fmaf(e.y, ptx::ex2(e.x - M), L);
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+        if (lane == 0) sm_lse[i] = M + log2f(L);
+        if (i % C != rank) continue;
+        constexpr int E = D / 32;  // columns E lane ..
+        float acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        for (int s0 = 0; s0 < a.NS; s0 += 8) {  // the loads of eight states in flight
+            float v[8][E];
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+                if (s0 + y < a.NS) ldcg_vec(a.o + (row * a.NS + s0 + y) * D + E * lane, v[y]);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                if (s0 + y >= a.NS) break;
+                const int s = s0 + y;
+                float f = __shfl_sync(0xffffffffu, f0, s & 31);
+                if (s >= 32) {
+                    const float m = __ldcg(ml + s).x;
+                    f = m == -INFINITY ? 0.f : ptx::ex2(m - M);
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(v[y][e], f, acc[e]);
+            }
+        }
+        for (int r = 0; r < C; ++r) {
+            const float f = __shfl_sync(0xffffffffu, cf, r);
+            float v[E];
+            cluster_ld_vec(cluster_addr(&join.o[0][i][E * lane], r), v);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(v[e], f, acc[e]);
+        }
+        uint32_t w[E / 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) w[e / 2] = pos < 0 ? 0u : ptx::pack_bf16x2(acc[e] / L, acc[e + 1] / L);
+        __nv_bfloat16* o = sa.out + row * D + E * lane;
+        if constexpr (E == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(o) = w[0];
+    }
+    if (C > 1) cluster_arrive();  // this CTA has read the others' states
+    if (SCORES) {
+        __syncthreads();
+        float* w = sa.weights + unit * a.S;
+        for (int s = r0 + tid; s < r1; s += kAttendWarps * 32) {
+            float p = 0.f;
+            for (int i = 0; i < nq; ++i) p += ptx::ex2(sm_z[i * a.chunk + s - r0] - sm_lse[i]);
+            w[s] += p;
+        }
+    }
+    if (C > 1) cluster_wait();
 }
 
 // ------------------------------------------------------------------ joining the splits
@@ -286,16 +465,18 @@ __global__ void __launch_bounds__(kFinishThreads)
         float acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
         for (int s = warp; s < a.NS; s += 4) {
             const float m = __ldcg(ml + s).x;
             if (m == -INFINITY) continue;
             const float f = ptx::ex2(m - all.x);
-            const float* op = a.o + (row * a.NS + s) * D + lane;
+            float v[E];
+            ldcg_vec(a.o + (row * a.NS + s) * D + E * lane, v);
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(__ldcg(op + 32 * e), f, acc[e]);
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(v[e], f, acc[e]);
         }
 #pragma unroll
-        for (int e = 0; e < E; ++e) sm[warp][lane + 32 * e] = acc[e];
+        for (int e = 0; e < E; ++e) sm[warp][E * lane + e] = acc[e];
         __syncthreads();
         if (tid < D) orow[tid] = __float2bfloat16_rn((sm[0][tid] + sm[1][tid] + sm[2][tid] + sm[3][tid]) / all.y);
         return;

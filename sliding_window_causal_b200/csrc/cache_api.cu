@@ -150,13 +150,16 @@ int launch_key_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const f
 }
 
 // ------------------------------------------------------------------ decode over slots and prefix
-// Splits of one call. The sizes alone decide them (148 SMs assumed), so a workspace query and a
-// call always agree.
+// How one call is split. The sizes alone decide it (148 SMs assumed), so a workspace query and
+// a call always agree.
 struct Plan {
-    int ns, chunk;    // the streams' slots
-    int np, pchunk;   // the prefix: partial states a row; keys a split takes (key tiles with tc)
-    bool tc, pair;    // the prefix on the tensor cores; two row tiles a CTA
-    int64_t NS;
+    int C;            // CTAs of a cluster of stream_kernel; 0: attend_kernel and finish_kernel
+    int P0, pchunk0;  // prefix keys that stream_kernel reads by itself (all or none); of a CTA
+    int ns, chunk;    // the streams' slots: splits; slots that a CTA takes
+    int np, pchunk;   // the rest of the prefix, by prefix_kernel: splits; key tiles that a CTA takes
+    bool pair;        // two row tiles a CTA
+    bool early;       // stream_kernel starts beside the prefix's kernel
+    int64_t NS;       // partial states a row in the workspace
     int64_t off_o, off_scores, bytes;  // workspace: (m, l), o, scores
 };
 
@@ -169,19 +172,17 @@ void split(int64_t units, int64_t keys, int* n, int* chunk) {
     *n = (int)((keys + c - 1) / c);
 }
 
-// The prefix on the tensor cores when more rows share its keys than one CTA of attend_kernel
-// serves.
-constexpr int64_t kPrefixTcRows = swa::kAttendQueries + 1;
-
 // Key tiles that a CTA of prefix_kernel takes, of `tiles`, when `groups` CTAs take them all: the
 // fewest rounds of 148 CTAs (one fits an SM) by the length of a round, where the start and end
-// of a CTA count as 3 tiles.
-int64_t prefix_chunk(int64_t groups, int64_t tiles) {
+// of a CTA count as 3 tiles and a further partial state to join as half a tile.
+int64_t prefix_chunk(int64_t groups, int64_t tiles, int64_t least) {
     int64_t best = tiles, cost = INT64_MAX;
     for (int64_t ns = 1; ns <= tiles && ns <= 148; ++ns) {
-        const int64_t chunk = (tiles + ns - 1) / ns, rounds = (groups * ((tiles + chunk - 1) / chunk) + 147) / 148;
-        if (rounds * (chunk + 3) < cost) {
-            cost = rounds * (chunk + 3);
+        int64_t chunk = (tiles + ns - 1) / ns;
+        if (chunk < least) chunk = least;
+        const int64_t splits = (tiles + chunk - 1) / chunk, rounds = (groups * splits + 147) / 148;
+        if (rounds * 2 * (chunk + 3) + splits < cost) {
+            cost = rounds * 2 * (chunk + 3) + splits;
             best = chunk;
         }
     }
@@ -190,23 +191,64 @@ int64_t prefix_chunk(int64_t groups, int64_t tiles) {
 
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
+// A prefix of at most this many bytes, taken once for each stream, is left to stream_kernel: the
+// streams read it from L2, which costs less than a launch of its own and a join. 8 key heads,
+// slots 200, D = 128, own and not: 16 streams P 300 (20 MB) 9.8 and 11.1 us, 32 streams (39 MB)
+// 12.8 and 11.6, 16 streams P 1000 (66 MB) 14.6 and 11.4. Where a key head has at most 8 rows,
+// prefix_kernel's tiles are nearly empty: 2 streams P 4000 (66 MB) 13.2 and 20.1, 8 streams P
+// 4000 (131 MB) 21.2 and 21.8.
+constexpr int64_t kOwnPrefixBytes = 24 << 20, kOwnPrefixBytesFewRows = 128 << 20;
+// Scores that a CTA of stream_kernel keeps in shared memory, in bytes.
+constexpr int64_t kClusterScores = 28 << 10;
+
 Plan plan(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D, bool scores) {
     Plan p = {};
-    const int64_t G = H / Hkv, Q = swa::kAttendQueries;
-    split(B * Hkv * ((G + Q - 1) / Q), S, &p.ns, &p.chunk);
-    p.tc = P > 0 && B * G >= kPrefixTcRows;
-    p.pair = B * G > 128;
-    if (p.tc) {
-        const int64_t tiles = (P + 127) / 128;
-        p.pchunk = (int)prefix_chunk(Hkv * (p.pair ? (B * G + 255) / 256 : 1), tiles);
-        p.np = (int)((tiles + p.pchunk - 1) / p.pchunk) * (p.pair ? 1 : 2);
-    } else if (P > 0) {
-        split(Hkv, P, &p.np, &p.pchunk);
+    const int64_t G = H / Hkv, Q = swa::kAttendQueries, units = B * Hkv;
+    if (G <= Q) {
+        const bool own = P > 0 && (B == 1 || units * P <= (B * G <= Q ? kOwnPrefixBytesFewRows : kOwnPrefixBytes) / (4 * D));
+        // The time of a call in the keys that a CTA takes meanwhile, by the measured rates of the
+        // listed sizes: rounds of resident CTAs (4 an SM for D = 128, 6 for 64; a round that is
+        // not full still takes 0.55 of its time, as its CTAs share the bandwidth among fewer), each
+        // its keys and 70 for its start and end, 40 for the barriers of a cluster. Of D = 128,
+        // S = 1000, 192 heads: 30.3, 20.8, 27.8, 30.1 us for C = 1, 2, 4, 8; 384 heads: 38.5,
+        // 48.5, 45.9, 59.4; S = 4096, 2048 heads: 680, 643, 662, 711. attend_kernel spreads over
+        // all SMs but its second launch costs 290: 16 heads of S = 4096 take 16.9 us, a cluster 14.4.
+        const double keys = (double)(S + (own ? P : 0)), slots = 148.0 * (D == 128 ? 4 : 6);
+        double best = 1.1 * units * keys / slots + 290;
+        for (int64_t C = 1; C <= 8; C *= 2) {
+            const int64_t chunk = (S + 16 * C - 1) / (16 * C) * 16;
+            if (scores && chunk * G * 4 > kClusterScores) continue;
+            const double rounds = units * C / slots, part = rounds - std::floor(rounds);
+            const double cost =
+                (std::floor(rounds) + (part > 0 && part < 0.55 ? 0.55 : part)) * (keys / C + 70) + (C > 1 ? 40 : 0);
+            if (cost < best) {
+                best = cost;
+                p.C = (int)C;
+                p.chunk = (int)chunk;
+                p.P0 = own ? (int)P : 0;
+                p.pchunk0 = own ? (int)((P + 16 * C - 1) / (16 * C) * 16) : 0;
+            }
+        }
     }
+    if (p.C == 0) split(units * ((G + Q - 1) / Q), S, &p.ns, &p.chunk);
+    int64_t prefix_ctas = 0;
+    if (P > p.P0) {
+        p.pair = B * G > 128;
+        const int64_t tiles = (P + 127) / 128, groups = Hkv * (p.pair ? (B * G + 255) / 256 : 1);
+        p.pchunk = (int)prefix_chunk(groups, tiles, p.pair ? 1 : 2);
+        p.np = (int)((tiles + p.pchunk - 1) / p.pchunk);
+        prefix_ctas = groups * p.np;
+    }
+    // Beside the prefix's kernel when that leaves half of the SMs free (24 streams of 32 heads, 4 to a
+    // key head, S 1000, P 2000, 64 CTAs: 26.0 us, 36.4 one after the other). An SM that has run it
+    // keeps its shared-memory split, with too little L1 for many loads in flight, until it is idle
+    // (64 streams, S 1024, P 8192, 128 CTAs: 224 us, 201 one after the other).
+    p.early = p.C > 0 && p.np > 0 && prefix_ctas <= 74;
     p.NS = p.ns + p.np;
     p.off_o = round256(B * H * p.NS * 8);
     p.off_scores = p.off_o + round256(B * H * p.NS * D * 4);
-    p.bytes = p.off_scores + (scores ? round256(B * H * S * 4) : 0);
+    p.bytes = p.off_scores + (scores && p.C == 0 ? round256(B * H * S * 4) : 0);
+    if (p.bytes < 256) p.bytes = 256;
     return p;
 }
 
@@ -233,7 +275,7 @@ int launch_prefix(const Plan& pl, const swa::AttendArgs& pre, cudaStream_t s) {
     if (int rc = swa_internal::tensor_map(&tm_k, pre.k, 1, pre.Hkv, P, D, ks, 128)) return rc;
     if (int rc = swa_internal::tensor_map(&tm_v, pre.v, 1, pre.Hkv, P, D, vs, 128)) return rc;
     const int64_t rows = (int64_t)pre.B * pre.G, groups = PAIR ? (rows + 255) / 256 : 1;
-    const dim3 grid((unsigned)(pre.Hkv * groups), (unsigned)(pl.np / (PAIR ? 1 : 2)));
+    const dim3 grid((unsigned)(pre.Hkv * groups), (unsigned)pl.np);
     kernel<<<grid, swa::kPrefixThreads, Cf::kSmemBytes, s>>>(tm_k, tm_v, pre, swa_internal::wait_limit_ns());
     return launched("prefix");
 }
@@ -244,14 +286,45 @@ int launch_decode(const Plan& pl, const swa::AttendArgs& ring, const swa::Attend
     const int Q = swa::kAttendQueries;
     const int64_t units = (int64_t)ring.B * ring.Hkv;
     const unsigned threads = swa::kAttendWarps * 32;
-    if (pl.tc) {
+    if (pl.np > 0)
         if (int rc = pl.pair ? launch_prefix<D, true>(pl, pre, s) : launch_prefix<D, false>(pl, pre, s)) return rc;
-    } else if (pl.np > 0) {
-        swa::attend_kernel<D, true, false><<<dim3((unsigned)ring.Hkv, (unsigned)pl.np), threads, 0, s>>>(pre);
+    if (pl.C > 0) {
+        swa::StreamArgs sa = {};
+        sa.a = ring;
+        sa.pk = pre.k;
+        sa.pv = pre.v;
+        sa.pk_head = pre.k_head;
+        sa.pk_row = pre.k_row;
+        sa.pv_head = pre.v_head;
+        sa.pv_row = pre.v_row;
+        sa.P0 = pl.P0;
+        sa.pchunk = pl.pchunk0;
+        sa.C = pl.C;
+        sa.out = out;
+        sa.weights = weights;
+        cudaLaunchConfig_t cfg = config(dim3((unsigned)(units * pl.C)), threads,
+                                        weights ? (size_t)pl.chunk * ring.G * 4 : 0, s);
+        cudaLaunchAttribute at[2];
+        unsigned n = 0;
+        if (pl.C > 1) {
+            at[n].id = cudaLaunchAttributeClusterDimension;
+            at[n].val.clusterDim.x = (unsigned)pl.C;
+            at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+            ++n;
+        }
+        if (pl.early) {
+            at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            at[n].val.programmaticStreamSerializationAllowed = 1;
+            ++n;
+        }
+        cfg.attrs = at;
+        cfg.numAttrs = n;
+        cudaLaunchKernelEx(&cfg, weights ? swa::stream_kernel<D, true> : swa::stream_kernel<D, false>, sa);
+        return SWA_OK;
     }
     const dim3 grid((unsigned)(units * ((ring.G + Q - 1) / Q)), (unsigned)pl.ns);
-    if (weights) swa::attend_kernel<D, false, true><<<grid, threads, 0, s>>>(ring);
-    else swa::attend_kernel<D, false, false><<<grid, threads, 0, s>>>(ring);
+    if (weights) swa::attend_kernel<D, true><<<grid, threads, 0, s>>>(ring);
+    else swa::attend_kernel<D, false><<<grid, threads, 0, s>>>(ring);
     const int slot_blocks = weights ? (ring.S + swa::kFinishSlots - 1) / swa::kFinishSlots : 0;
     const int64_t blocks = (int64_t)ring.B * ring.H + units * slot_blocks;
     launch_after(dim3((unsigned)blocks), swa::kFinishThreads, (size_t)ring.G * 4, s, swa::finish_kernel<D>, ring, out,
@@ -284,7 +357,7 @@ int decode(const char* fn, const void* q, const void* k, const void* v, const in
     }
     const int64_t G = H / Hkv;
     const int64_t blocks = B * H + (scores ? B * Hkv * ((S + swa::kFinishSlots - 1) / swa::kFinishSlots) : 0);
-    if (blocks > INT32_MAX || pl.ns > 65535) return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    if (blocks > INT32_MAX || B * Hkv > INT32_MAX / 8 || pl.ns > 65535) return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     int *status, num_sms;
     if (int rc = swa_internal::device_info(&status, &num_sms)) return rc;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -304,7 +377,7 @@ int decode(const char* fn, const void* q, const void* k, const void* v, const in
     a.G = (int)G;
     a.S = (int)S;
     a.chunk = pl.chunk;
-    a.split0 = pl.np;
+    a.split0 = pl.np;  // the prefix's partial states come first
     a.NS = (int)pl.NS;
     a.scale_log2 = (float)(1.4426950408889634 * scale);
     a.status = status;

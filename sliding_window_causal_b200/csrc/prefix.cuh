@@ -9,8 +9,8 @@
 // of TMEM and its softmax warpgroup:
 //   PAIR   (more than 128 rows a key head) lane x has row tile x and takes every key tile, so
 //          that a key tile in shared memory serves 256 rows;
-//   !PAIR  both lanes have the one row tile and take every second key tile, as splits of their
-//          own: with up to 128 rows the prefix's bytes bound the call, and one lane's chain
+//   !PAIR  (fewer) both lanes have the one row tile and take every second key tile, and join at the end:
+//          with up to 128 rows the prefix's bytes bound the call, and one lane's chain
 //          S -> softmax -> P V would be too slow to ask for them.
 // While one lane is in its softmax the tensor core works for the other. Roles: warp 0 TMA
 // producer (K and V tiles through one ring), warp 1 MMA issuer, warps 4 .. 7 and 8 .. 11 the
@@ -124,7 +124,7 @@ __device__ __forceinline__ void prefix_tile(uint32_t scol, uint32_t ocol, float 
 }
 
 // a: q, ml, o, B, H, Hkv, G, S (prefix length), chunk (key tiles a split takes), NS, scale_log2
-// and status are read. Partial states of split s: index s (PAIR), 2 s + lane (!PAIR).
+// and status are read. Split s writes the partial states of index s.
 template <int D, bool PAIR>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const AttendArgs a,
@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const int hk = (int)blockIdx.x / groups, row0 = ((int)blockIdx.x % groups) * kRows;
     const int t0 = (int)blockIdx.y * a.chunk, tiles = (a.S + 127) / 128;
     const int n = min(a.chunk, tiles - t0);  // key tiles of this CTA, at least 1
+    ptx::launch_dependents();
 
     if (threadIdx.x == 0) {
         ptx::mbar_init(q_full, 4 * Cf::kQTiles);
@@ -336,27 +337,69 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             if (last >= 127) prefix_tile<D, false, LO>(scol, ocol, a.scale_log2, m, l, 127, after_part);
             else prefix_tile<D, true, LO>(scol, ocol, a.scale_log2, m, l, last, after_part);
         }
-        const int64_t at = qrow * a.NS + (PAIR ? (int)blockIdx.y : 2 * (int)blockIdx.y + x);
-        if (ok && mine > 0)
-            ok = __all_sync(0xffffffffu, ptx::mbar_wait(o_final + x, 0, wait_limit_ns, abort_flag));
-        if (ok && mine > 0) {
-            ptx::tc_fence_after();
+        const int64_t at = qrow * a.NS + (int)blockIdx.y;
+        if (PAIR) {
+            if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(o_final + x, 0, wait_limit_ns, abort_flag));
+            if (ok) {
+                ptx::tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                ptx::tmem_ld32(ocol + 32 * c, o);
-                ptx::tmem_ld_wait();
-                ptx::reg_fence(o);
-                if (live) {
-                    float4* to = reinterpret_cast<float4*>(a.o + at * D + 32 * c);
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    ptx::tmem_ld32(ocol + 32 * c, o);
+                    ptx::tmem_ld_wait();
+                    ptx::reg_fence(o);
+                    if (live) {
+                        float4* to = reinterpret_cast<float4*>(a.o + at * D + 32 * c);
 #pragma unroll
-                    for (int t = 0; t < 8; ++t)
-                        to[t] = make_float4(__uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]),
-                                            __uint_as_float(o[4 * t + 2]), __uint_as_float(o[4 * t + 3]));
+                        for (int t = 0; t < 8; ++t)
+                            to[t] = make_float4(__uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]),
+                                                __uint_as_float(o[4 * t + 2]), __uint_as_float(o[4 * t + 3]));
+                    }
                 }
             }
+            if (live) a.ml[at] = make_float2(m, l);
+        } else {
+            // The two lanes' states of a row become one: O_0 and O_1 are in the same TMEM lanes, so
+            // each warpgroup joins half of the columns; m and l cross through shared memory (the
+            // ring's first bytes: its tiles are read once both lanes' O is final).
+            for (int y = 0; y < 2 && y < n; ++y)
+                if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(o_final + y, 0, wait_limit_ns, abort_flag));
+            float2* sm_ml = reinterpret_cast<float2*>(smem + Cf::kRingOff);  // [2][128]
+            if (ok) sm_ml[128 * x + row] = make_float2(m, l);
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (ok) {
+                ptx::tc_fence_after();
+                const float2 other = sm_ml[128 * (1 - x) + row];
+                const float M = fmaxf(m, other.x);
+                const float mine_f = m == -INFINITY ? 0.f : ptx::ex2(m - M);
+                const float other_f = other.x == -INFINITY ? 0.f : ptx::ex2(other.x - M);
+                const float f0 = x ? other_f : mine_f, f1 = x ? mine_f : other_f;
+#pragma unroll 1
+                for (int c = x * (D / 64); c < (x + 1) * (D / 64); ++c) {
+                    uint32_t o[2][32];
+                    ptx::tmem_ld32(tl + Cf::colO(0) + 32 * c, o[0]);
+                    ptx::tmem_ld32(tl + Cf::colO(1) + 32 * c, o[1]);
+                    ptx::tmem_ld_wait();
+                    ptx::reg_fence(o[0]);
+                    ptx::reg_fence(o[1]);
+                    if (live) {
+                        float4* to = reinterpret_cast<float4*>(a.o + at * D + 32 * c);
+#pragma unroll
+                        for (int t = 0; t < 8; ++t) {
+                            float v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                // with one key tile O_1 was never written
+                                const float o1 = n > 1 ? __uint_as_float(o[1][4 * t + e]) * f1 : 0.f;
+                                v[e] = fmaf(__uint_as_float(o[0][4 * t + e]), f0, o1);
+                            }
+                            to[t] = make_float4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
+                }
+                if (live && x == 0) a.ml[at] = make_float2(M, fmaf(l, f0, other.y * f1));
+            }
         }
-        if (live) a.ml[at] = make_float2(m, l);  // a lane without a key tile: (-inf, 0)
         if (!ok) {
             atomicCAS(a.status, 0, 5);
             *abort_flag = 1;
