@@ -440,8 +440,9 @@ int swa_cache_append(const void* k, const void* v, void* kcache, void* vcache, f
  *   kprefix, vprefix : [Hkv,P,D] bf16; strides NULL (contiguous) or 4 element strides k(h,t),
  *                      v(h,t). With P = 0 they and the strides are not read.
  *   workspace        : caller-owned, workspace_bytes >= swa_cache_decode_workspace_bytes bytes,
- *                      256-byte aligned; its contents need no preparation and mean nothing
- *                      afterwards. Calls that may run at the same time need their own.
+ *                      256-byte aligned (NULL if that is 0); its contents need no preparation
+ *                      and mean nothing afterwards. Calls that may run at the same time need
+ *                      their own.
  *   scale            : of the scores, > 0.      D : 64 or 128.
  * Scores, statistics and sums are fp32. A negative pos[b] is found on the device: that stream's
  * output is zeros, its weights stay and swa_device_status() reports SWA_ERR_INVALID_ARG.
@@ -452,7 +453,8 @@ int swa_cache_decode(const void* q, const void* kcache, const void* vcache, floa
                      int64_t workspace_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D,
                      double scale, const int64_t* strides, void* stream);
 
-/* swa_cache_decode_workspace_bytes: bytes of workspace for these sizes, or -1 for invalid ones. */
+/* swa_cache_decode_workspace_bytes: bytes of workspace for these sizes (0: none), or
+ * -1 for invalid ones. */
 int64_t swa_cache_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D);
 
 /*
@@ -472,7 +474,8 @@ int swa_prefix_decode(const void* q, const void* kprefix, const void* vprefix, c
                       int64_t B, int64_t H, int64_t Hkv, int64_t W, int64_t P, int64_t D, double scale,
                       const int64_t* strides, void* stream);
 
-/* swa_prefix_decode_workspace_bytes: bytes of workspace for these sizes, or -1 for invalid ones. */
+/* swa_prefix_decode_workspace_bytes: bytes of workspace for these sizes (0: none), or
+ * -1 for invalid ones. */
 int64_t swa_prefix_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t W, int64_t P, int64_t D);
 
 /* ---- Host-side work planning (no GPU needed; the kernels use the same code) ---- */

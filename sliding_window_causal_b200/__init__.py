@@ -343,6 +343,31 @@ def forward_host(q, k, v, window, out=None, device=None, staging=None, heads_per
     return out
 
 
+def _same_device(dense, strided=()):
+    """The index of the device that holds all of these tensors: `dense` contiguous, `strided` with
+    a contiguous head dimension."""
+    d = dense[0].get_device()
+    for t in dense:
+        if t.get_device() != d or d < 0 or not t.is_contiguous():
+            _need_cuda(dense[0], t)  # says what is wrong
+    for t in strided:
+        if t.get_device() != d:
+            _need_cuda(dense[0], t, contiguous=False)
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            _need_cuda(t, contiguous=False)
+    return d
+
+
+def _launch(index, fn, *args):
+    """fn(*args, current stream) with device `index` as the current one."""
+    torch = _torch()
+    if index == torch.cuda.current_device():
+        check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+    else:
+        with torch.cuda.device(index):
+            check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+
+
 def _heads(H, Hkv):
     if Hkv < 1 or H % Hkv:
         raise ValueError(f"{H} query heads are not a multiple of {Hkv} key heads")
@@ -350,18 +375,8 @@ def _heads(H, Hkv):
 
 def _positions(pos, B, name="pos"):
     torch = _torch()
-    if pos.shape != (B,) or pos.dtype != torch.int64:
+    if pos.dtype != torch.int64 or pos.shape != (B,):
         raise ValueError(f"{name} must be int64 [B]")
-
-
-def _launch(dev, fn, *args):
-    """fn(*args, current stream of dev) with dev the current device."""
-    torch = _torch()
-    if dev.index == torch.cuda.current_device():
-        check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
-    else:
-        with torch.cuda.device(dev):
-            check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
 
 
 def key_weights(q, k, lse, window, lens=None, last=None, scale=None):
@@ -380,33 +395,33 @@ def key_weights(q, k, lse, window, lens=None, last=None, scale=None):
     B, H, T, D = q.shape
     Hkv = k.shape[1]
     _heads(H, Hkv)
-    if lse.shape != (B, H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    if lse.dtype != torch.float32 or lse.shape != (B, H, T) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [B,H,T]")
-    dev = _need_cuda(q, k, lse, contiguous=False)
     if lens is not None:
         _positions(lens, B, "lens")
-        _need_cuda(q, lens, contiguous=False)
-        lens = lens.contiguous()
-    out = torch.empty((B, Hkv, T), dtype=torch.float32, device=dev)
+    dev = _same_device((lse,) if lens is None else (lse, lens), (q, k))
+    out = torch.empty((B, Hkv, T), dtype=torch.float32, device=q.device)
     sc = 1.0 / D ** 0.5 if scale is None else float(scale)
+    strides = None if q.is_contiguous() and k.is_contiguous() else _bht_strides(q, k)
     _launch(dev, _native.lib().swa_key_weights, q.data_ptr(), k.data_ptr(), lse.data_ptr(),
             None if lens is None else lens.data_ptr(), out.data_ptr(), B, H, Hkv, T, D, int(window),
-            max(T, 1) if last is None else int(last), sc, _bht_strides(q, k), _dtype_code(q))
+            max(T, 1) if last is None else int(last), sc, strides, _dtype_code(q))
     return out
 
 
 def _budget_cache(kcache, vcache, wcache, pcache):
     """(B, Hkv, S, D) of a budget cache; pcache may be None."""
     torch = _torch()
-    if kcache.dim() != 4 or vcache.shape != kcache.shape:
+    shape = kcache.shape
+    if len(shape) != 4 or vcache.shape != shape:
         raise ValueError("kcache and vcache must share one [B,Hkv,S,D] shape")
     if kcache.dtype != torch.bfloat16 or vcache.dtype != torch.bfloat16:
         raise TypeError("the cache's keys and values are bf16")
-    if wcache.shape != kcache.shape[:3] or wcache.dtype != torch.float32:
+    if wcache.dtype != torch.float32 or wcache.shape != shape[:3]:
         raise ValueError("wcache must be fp32 [B,Hkv,S]")
-    if pcache is not None and (pcache.shape != kcache.shape[:3] or pcache.dtype != torch.int64):
+    if pcache is not None and (pcache.dtype != torch.int64 or pcache.shape != shape[:3]):
         raise ValueError("pcache must be int64 [B,Hkv,S]")
-    return kcache.shape
+    return shape
 
 
 def cache_seed(k, v, weights, kcache, vcache, wcache, pcache, recent, lens=None):
@@ -423,16 +438,17 @@ def cache_seed(k, v, weights, kcache, vcache, wcache, pcache, recent, lens=None)
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
         raise TypeError("the cache's keys and values are bf16")
     T = k.shape[2]
-    if weights.shape != (B, Hkv, T) or weights.dtype != torch.float32:
+    if weights.dtype != torch.float32 or weights.shape != (B, Hkv, T):
         raise ValueError("weights must be fp32 [B,Hkv,T]")
-    dev = _need_cuda(kcache, vcache, wcache, pcache, weights)
-    _need_cuda(kcache, k, v, contiguous=False)
+    dense = (kcache, vcache, wcache, pcache, weights)
     if lens is not None:
         _positions(lens, B, "lens")
-        _need_cuda(kcache, lens)
+        dense += (lens,)
+    dev = _same_device(dense, (k, v))
+    strides = None if k.is_contiguous() and v.is_contiguous() else _bht_strides(k, v)
     _launch(dev, _native.lib().swa_cache_seed, k.data_ptr(), v.data_ptr(), weights.data_ptr(),
             None if lens is None else lens.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), wcache.data_ptr(),
-            pcache.data_ptr(), B, Hkv, T, D, S, int(recent), _bht_strides(k, v))
+            pcache.data_ptr(), B, Hkv, T, D, S, int(recent), strides)
 
 
 def cache_append(k, v, kcache, vcache, wcache, pcache, pos, recent):
@@ -448,45 +464,65 @@ def cache_append(k, v, kcache, vcache, wcache, pcache, pos, recent):
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
         raise TypeError("the cache's keys and values are bf16")
     _positions(pos, B)
-    dev = _need_cuda(k, v, kcache, vcache, wcache, pcache, pos)
-    slots = torch.empty((B, Hkv), dtype=torch.int64, device=dev)
+    dev = _same_device((k, v, kcache, vcache, wcache, pcache, pos))
+    slots = torch.empty((B, Hkv), dtype=torch.int64, device=k.device)
     _launch(dev, _native.lib().swa_cache_append, k.data_ptr(), v.data_ptr(), kcache.data_ptr(), vcache.data_ptr(),
             wcache.data_ptr(), pcache.data_ptr(), pos.data_ptr(), slots.data_ptr(), B, Hkv, D, S, int(recent))
     return slots
 
 
-def _prefix(kprefix, vprefix, Hkv, D):
-    """(P, kprefix pointer, vprefix pointer, strides) of a shared prefix, or of none."""
+def _decode(fn, need, weighted, q, kc, vc, wc, pos, kprefix, vprefix, S, Hkv, out, scale, workspace):
+    """The two decodes' common part: prefix, buffers and call."""
     torch = _torch()
+    B, H, D = q.shape
+    _heads(H, Hkv)
+    _positions(pos, B)
     if (kprefix is None) != (vprefix is None):
         raise ValueError("give both kprefix and vprefix, or neither")
-    if kprefix is None:
-        return 0, None, None, None
-    if kprefix.dim() != 3 or vprefix.shape != kprefix.shape or (kprefix.shape[0], kprefix.shape[2]) != (Hkv, D):
-        raise ValueError("kprefix and vprefix must share one [Hkv,P,D] shape")
-    if kprefix.dtype != torch.bfloat16 or vprefix.dtype != torch.bfloat16:
-        raise TypeError("the prefix is bf16")
-    st = (*kprefix.stride()[:2], *vprefix.stride()[:2])
-    return kprefix.shape[1], kprefix.data_ptr(), vprefix.data_ptr(), (ctypes.c_int64 * 4)(*st)
-
-
-def _decode_out(q, out, workspace, need, dev):
-    torch = _torch()
+    dense = [q, kc, vc, pos]
+    if weighted:
+        dense.append(wc)
+    P, kp, vp, strides, prefix = 0, None, None, None, ()
+    if kprefix is not None:
+        if kprefix.dim() != 3 or vprefix.shape != kprefix.shape or (kprefix.shape[0], kprefix.shape[2]) != (Hkv, D):
+            raise ValueError("kprefix and vprefix must share one [Hkv,P,D] shape")
+        if kprefix.dtype != torch.bfloat16 or vprefix.dtype != torch.bfloat16:
+            raise TypeError("the prefix is bf16")
+        P = kprefix.shape[1]
+        if P:
+            prefix = (kprefix, vprefix)
+            kp, vp = kprefix.data_ptr(), vprefix.data_ptr()
+            if not (kprefix.is_contiguous() and vprefix.is_contiguous()):
+                strides = (ctypes.c_int64 * 4)(*kprefix.stride()[:2], *vprefix.stride()[:2])
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     else:
-        _need_cuda(q, out)
         if out.shape != q.shape or out.dtype != q.dtype:
             raise ValueError("out must match q")
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        dense.append(out)
+    if workspace is not None:
+        dense.append(workspace)
+    dev = _same_device(dense, prefix)
+    ws, have = None, 0
+    if workspace is not None:
+        ws, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     else:
-        _need_cuda(q, workspace)
-    return out, workspace, workspace.numel() * workspace.element_size()
+        have = need(B, H, Hkv, S, P, D)
+        if have > 0:
+            workspace = torch.empty(have, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
+    sc = 1.0 / D ** 0.5 if scale is None else float(scale)
+    cache = (kc.data_ptr(), vc.data_ptr())
+    if weighted:
+        args = (q.data_ptr(), *cache, wc.data_ptr(), pos.data_ptr(), kp, vp)
+    else:
+        args = (q.data_ptr(), kp, vp, *cache, pos.data_ptr())
+    _launch(dev, fn, *args, out.data_ptr(), ws, have, B, H, Hkv, S, P, D, sc, strides)
+    return out
 
 
 def cache_decode_workspace_bytes(B, H, Hkv, S, P, D):
-    """Bytes of device workspace cache_decode needs."""
+    """Bytes of device workspace cache_decode needs (0: none)."""
     return int(_native.lib().swa_cache_decode_workspace_bytes(B, H, Hkv, S, P, D))
 
 
@@ -504,24 +540,13 @@ def cache_decode(q, kcache, vcache, wcache, pos, kprefix=None, vprefix=None, out
         raise ValueError("q must be [B,H,D] and the cache [B,Hkv,S,D]")
     if q.dtype != torch.bfloat16:
         raise TypeError("cache_decode takes bf16 q")
-    H = q.shape[1]
-    _heads(H, Hkv)
-    _positions(pos, B)
-    P, kp, vp, strides = _prefix(kprefix, vprefix, Hkv, D)
-    dev = _need_cuda(q, kcache, vcache, wcache, pos)
-    if P:
-        _need_cuda(q, kprefix, vprefix, contiguous=False)
     lib = _native.lib()
-    need = lib.swa_cache_decode_workspace_bytes(B, H, Hkv, S, P, D)
-    out, workspace, have = _decode_out(q, out, workspace, need, dev)
-    sc = 1.0 / D ** 0.5 if scale is None else float(scale)
-    _launch(dev, lib.swa_cache_decode, q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), wcache.data_ptr(),
-            pos.data_ptr(), kp, vp, out.data_ptr(), workspace.data_ptr(), have, B, H, Hkv, S, P, D, sc, strides)
-    return out
+    return _decode(lib.swa_cache_decode, lib.swa_cache_decode_workspace_bytes, True, q, kcache, vcache, wcache, pos,
+                   kprefix, vprefix, S, Hkv, out, scale, workspace)
 
 
 def prefix_decode_workspace_bytes(B, H, Hkv, W, P, D):
-    """Bytes of device workspace prefix_decode needs."""
+    """Bytes of device workspace prefix_decode needs (0: none)."""
     return int(_native.lib().swa_prefix_decode_workspace_bytes(B, H, Hkv, W, P, D))
 
 
@@ -536,25 +561,14 @@ def prefix_decode(q, kprefix, vprefix, kring, vring, pos, window, out=None, scal
     torch = _torch()
     if q.dim() != 3 or kring.dim() != 4:
         raise ValueError("q must be [B,H,D] and the rings [B,Hkv,W,D]")
-    B, H, D = q.shape
     Hkv = kring.shape[1]
-    if kring.shape != (B, Hkv, window, D) or vring.shape != kring.shape:
+    if kring.shape != (q.shape[0], Hkv, window, q.shape[2]) or vring.shape != kring.shape:
         raise ValueError("rings must be [B,Hkv,W,D] with W = window")
     if q.dtype != torch.bfloat16 or kring.dtype != torch.bfloat16 or vring.dtype != torch.bfloat16:
         raise TypeError("prefix_decode takes bf16 q and rings")
-    _heads(H, Hkv)
-    _positions(pos, B)
-    P, kp, vp, strides = _prefix(kprefix, vprefix, Hkv, D)
-    dev = _need_cuda(q, kring, vring, pos)
-    if P:
-        _need_cuda(q, kprefix, vprefix, contiguous=False)
     lib = _native.lib()
-    need = lib.swa_prefix_decode_workspace_bytes(B, H, Hkv, window, P, D)
-    out, workspace, have = _decode_out(q, out, workspace, need, dev)
-    sc = 1.0 / D ** 0.5 if scale is None else float(scale)
-    _launch(dev, lib.swa_prefix_decode, q.data_ptr(), kp, vp, kring.data_ptr(), vring.data_ptr(), pos.data_ptr(),
-            out.data_ptr(), workspace.data_ptr(), have, B, H, Hkv, int(window), P, D, sc, strides)
-    return out
+    return _decode(lib.swa_prefix_decode, lib.swa_prefix_decode_workspace_bytes, False, q, kring, vring, None, pos,
+                   kprefix, vprefix, int(window), Hkv, out, scale, workspace)
 
 
 def device_status(stream=None):

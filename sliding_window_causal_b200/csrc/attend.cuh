@@ -278,24 +278,6 @@ struct StreamArgs {
     float* weights;
 };
 
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(ptx::smem_u32(p)), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ float cluster_ld(uint32_t at) {
-    float x;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at));
-    return x;
-}
-__device__ __forceinline__ void cluster_ld_vec(uint32_t at, float (&v)[4]) {
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-                 : "r"(at));
-}
-__device__ __forceinline__ void cluster_ld_vec(uint32_t at, float (&v)[2]) {
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(at));
-}
 __device__ __forceinline__ void ldcg_vec(const float* p, float (&v)[4]) {
     const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
     v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
@@ -304,8 +286,6 @@ __device__ __forceinline__ void ldcg_vec(const float* p, float (&v)[2]) {
     const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
     v[0] = x.x; v[1] = x.y;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 template <int D, bool SCORES>
 __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_kernel(const StreamArgs sa) {
@@ -342,8 +322,8 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_ke
         }
     });
     if (C > 1) {
-        cluster_arrive();
-        cluster_wait();
+        ptx::cluster_arrive();
+        ptx::cluster_wait();
     } else {
         __syncthreads();
     }
@@ -353,8 +333,8 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_ke
         const float2* ml = a.ml + row * a.NS;
         float cm = -INFINITY, cl = 0.f;  // lane: the state of CTA `lane`
         if (lane < C) {
-            cm = cluster_ld(cluster_addr(&sm_m[i], lane));
-            cl = cluster_ld(cluster_addr(&sm_l[i], lane));
+            cm = ptx::cluster_ld(ptx::cluster_addr(&sm_m[i], lane));
+            cl = ptx::cluster_ld(ptx::cluster_addr(&sm_l[i], lane));
         }
         // the prefix's: of a lane, state `lane` of every 32 (the first 32 stay in registers)
         const float2 e0 = lane < a.NS ? __ldcg(ml + lane) : make_float2(-INFINITY, 0.f);
@@ -397,7 +377,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_ke
         for (int r = 0; r < C; ++r) {
             const float f = __shfl_sync(0xffffffffu, cf, r);
             float v[E];
-            cluster_ld_vec(cluster_addr(&join.o[0][i][E * lane], r), v);
+            ptx::cluster_ld_vec(ptx::cluster_addr(&join.o[0][i][E * lane], r), v);
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[e] = fmaf(v[e], f, acc[e]);
         }
@@ -408,7 +388,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_ke
         if constexpr (E == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
         else *reinterpret_cast<uint32_t*>(o) = w[0];
     }
-    if (C > 1) cluster_arrive();  // this CTA has read the others' states
+    if (C > 1) ptx::cluster_arrive();  // this CTA has read the others' states
     if (SCORES) {
         __syncthreads();
         float* w = sa.weights + unit * a.S;
@@ -418,7 +398,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_ke
             w[s] += p;
         }
     }
-    if (C > 1) cluster_wait();
+    if (C > 1) ptx::cluster_wait();
 }
 
 // ------------------------------------------------------------------ joining the splits

@@ -23,8 +23,11 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 // ------------------------------------------------------------------ append
-// One CTA per (b, hk). Bound by the 12 bytes a slot (weight, position) that the choice reads.
-__global__ void __launch_bounds__(1024)
+// One CTA per (b, hk). Bound by the 12 bytes a slot (weight, position) that the choice reads;
+// the loads of kAppendUnroll slots a thread are in flight together.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendUnroll = 4;
+__global__ void __launch_bounds__(kAppendThreads, 6)
     cache_append_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v, uint4* __restrict__ kc,
                         uint4* __restrict__ vc, float* __restrict__ wc, int64_t* __restrict__ pc,
                         const int64_t* __restrict__ pos, int64_t* __restrict__ slots, int Hkv, int S, int recent,
@@ -41,13 +44,23 @@ __global__ void __launch_bounds__(1024)
         // the lightest candidate as (weight key, slot), and the slot that holds P already
         unsigned long long best = ~0ull;
         int same = INT32_MAX;
-        for (int s = tid; s < S; s += nt) {
-            const int64_t q = p[s];
-            const float x = w[s];
-            if (q == P) same = min(same, s);
-            if (q <= P - recent) {
-                const unsigned long long e = ((unsigned long long)weight_key(x) << 32) | (uint32_t)s;
-                best = e < best ? e : best;
+        for (int s0 = tid; s0 < S; s0 += kAppendUnroll * nt) {
+            int64_t q[kAppendUnroll];
+            float x[kAppendUnroll];
+#pragma unroll
+            for (int u = 0; u < kAppendUnroll; ++u) {
+                const int s = s0 + u * nt;
+                q[u] = s < S ? p[s] : INT64_MAX;
+                x[u] = s < S ? w[s] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < kAppendUnroll; ++u) {
+                const int s = s0 + u * nt;
+                if (q[u] == P && s < S) same = min(same, s);
+                if (q[u] <= P - recent && s < S) {
+                    const unsigned long long e = ((unsigned long long)weight_key(x[u]) << 32) | (uint32_t)s;
+                    best = e < best ? e : best;
+                }
             }
         }
 #pragma unroll
@@ -104,125 +117,171 @@ __device__ __forceinline__ int stream_len(const int64_t* lens, int64_t b, int T,
     return -1;
 }
 
-constexpr int kSeedThreads = 1024;
+constexpr int kSeedThreads = 512;
 
-// One CTA per (b, hk) chooses the positions its cache keeps and writes them, ascending, with
-// their weights. The newest `recent` are kept; of the older ones the need = S - recent
-// heaviest, found by a radix selection of the weight keys, 8 bits a pass: the keys above the
-// threshold, and of those equal to it the first few.
+// A cluster of C CTAs (1 <= C <= 8) per (b, hk) chooses the positions its cache keeps, writes
+// them, ascending, with their weights, and copies their rows. The newest `recent` are kept; of
+// the older ones the need = S - recent heaviest, found by a radix selection of the weight keys, 8
+// bits a pass: the keys above the threshold, and of those equal to it the first few. Each CTA
+// counts the digits of its run of positions; the counts meet in distributed shared memory. The
+// copy, 4 D bytes read and written a slot, is the bound; the passes over 4 bytes a position come
+// before it, which is why they are spread over a cluster.
 __global__ void __launch_bounds__(kSeedThreads)
-    seed_select_kernel(const float* __restrict__ weights, const int64_t* __restrict__ lens, float* __restrict__ wc,
-                       int64_t* __restrict__ pc, int Hkv, int T, int S, int recent, int* status) {
-    __shared__ int hist[256];
-    __shared__ int sm_a[32], sm_b[32];
+    cache_seed_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
+                      const float* __restrict__ weights, const int64_t* __restrict__ lens, uint4* __restrict__ kc,
+                      uint4* __restrict__ vc, float* __restrict__ wc, int64_t* pc, int64_t ksb, int64_t ksh, int64_t kst,
+                      int64_t vsb, int64_t vsh, int64_t vst, int Hkv, int T, int S, int recent, int vpr, int C,
+                      int* status) {
+    constexpr int kWarps = kSeedThreads / 32;
+    __shared__ int hist[2][256];  // of the even and the odd passes
+    __shared__ int all[256];      // the cluster's counts
+    __shared__ int sm_a[kWarps], sm_b[kWarps];
+    __shared__ int sm_cta[2];     // this CTA's keys above and equal to the threshold
     __shared__ uint32_t sm_prefix;
     __shared__ int sm_need;
-    const int64_t bh = blockIdx.x;
+    const int rank = (int)(blockIdx.x % C);
+    const int64_t bh = blockIdx.x / C, b = bh / Hkv, h = bh - b * Hkv;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int n = stream_len(lens, bh / Hkv, T, status);
+    const int n = stream_len(lens, b, T, status);
     const float* w = weights + bh * T;
     float* wo = wc + bh * S;
     int64_t* po = pc + bh * S;
-    if (n <= S) {
-        for (int j = tid; j < n; j += kSeedThreads) {
+    auto sync = [&] {  // the cluster's CTAs, or this one's threads
+        if (C > 1) {
+            ptx::cluster_arrive();
+            ptx::cluster_wait();
+        } else {
+            __syncthreads();
+        }
+    };
+    if (n > S) {
+        const int old = n - recent;  // positions 0 .. old-1 compete for S - recent slots; old > need
+        const int run = ((old + C - 1) / C + 31) / 32 * 32;  // this CTA's: c0 .. c1-1
+        const int c0 = min(old, rank * run), c1 = min(old, c0 + run);
+        int need = S - recent;
+        uint32_t prefix = 0;
+        for (int pass = 0; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass;
+            const uint32_t mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
+            int* mine = hist[pass & 1];
+            if (tid < 256) mine[tid] = 0;
+            __syncthreads();
+            for (int j = c0 + tid; j < c1; j += kSeedThreads) {
+                const uint32_t key = weight_key(w[j]);
+                if ((key & mask) == prefix) atomicAdd(&mine[(key >> shift) & 255], 1);
+            }
+            sync();
+            if (tid < 256) {
+                int sum = 0;
+                if (C > 1)
+                    for (int r = 0; r < C; ++r) sum += __float_as_int(ptx::cluster_ld(ptx::cluster_addr(&mine[tid], r)));
+                else sum = mine[tid];
+                all[tid] = sum;
+            }
+            __syncthreads();
+            if (warp == 0) {  // the digit at which the count from above reaches need
+                int own[8], sum = 0;  // lane: digits 255 - 8 lane - i
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum += own[i] = all[255 - 8 * lane - i];
+                int incl = sum;
+#pragma unroll
+                for (int x = 1; x < 32; x <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, incl, x);
+                    if (lane >= x) incl += y;
+                }
+                int before = incl - sum;
+                if (before < need && need <= incl) {
+                    int i = 0;
+                    while (before + own[i] < need) before += own[i++];
+                    sm_prefix = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
+                    sm_need = need - before;
+                }
+            }
+            __syncthreads();
+            prefix = sm_prefix;
+            need = sm_need;
+            // The next pass clears the other histogram: every CTA has read that one, as it has
+            // passed this pass's cluster barrier since.
+        }
+        // Keep keys > prefix and the first `need` keys equal to it. Each warp takes one run of
+        // positions; the counts of the warps and CTAs before it say where its own go.
+        const int wrun = ((c1 - c0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+        const int j0 = min(c1, c0 + warp * wrun), j1 = min(c1, j0 + wrun);
+        int above = 0, equal = 0;
+        for (int j = j0 + lane; j - lane < j1; j += 32) {
+            const uint32_t key = j < j1 ? weight_key(w[j]) : 0u;
+            above += __popc(__ballot_sync(0xffffffffu, j < j1 && key > prefix));
+            equal += __popc(__ballot_sync(0xffffffffu, j < j1 && key == prefix));
+        }
+        if (lane == 0) {
+            sm_a[warp] = above;
+            sm_b[warp] = equal;
+        }
+        __syncthreads();
+        if (tid < 2) {
+            int sum = 0;
+            for (int x = 0; x < kWarps; ++x) sum += tid ? sm_b[x] : sm_a[x];
+            sm_cta[tid] = sum;
+        }
+        sync();
+        int na = 0, ne = 0;  // kept above and seen equal before this position
+        for (int r = 0; r < rank; ++r) {
+            na += __float_as_int(ptx::cluster_ld(ptx::cluster_addr(&sm_cta[0], r)));
+            ne += __float_as_int(ptx::cluster_ld(ptx::cluster_addr(&sm_cta[1], r)));
+        }
+        for (int x = 0; x < warp; ++x) {
+            na += sm_a[x];
+            ne += sm_b[x];
+        }
+        const uint32_t below = (1u << lane) - 1u;
+        for (int j = j0 + lane; j - lane < j1; j += 32) {
+            const float x = j < j1 ? w[j] : 0.f;
+            const uint32_t key = weight_key(x);
+            const uint32_t ba = __ballot_sync(0xffffffffu, j < j1 && key > prefix);
+            const uint32_t be = __ballot_sync(0xffffffffu, j < j1 && key == prefix);
+            const int a = na + __popc(ba & below), e = ne + __popc(be & below);
+            if (j < j1 && (key > prefix || (key == prefix && e < need))) {
+                const int at = a + min(e, need);
+                wo[at] = x;
+                po[at] = j;
+            }
+            na += __popc(ba);
+            ne += __popc(be);
+        }
+        for (int i = rank * kSeedThreads + tid; i < recent; i += C * kSeedThreads) {
+            wo[S - recent + i] = w[old + i];
+            po[S - recent + i] = old + i;
+        }
+    } else {
+        for (int j = rank * kSeedThreads + tid; j < n; j += C * kSeedThreads) {
             wo[j] = w[j];
             po[j] = j;
         }
-        return;
     }
-    const int old = n - recent;  // positions 0 .. old-1 compete for S - recent slots; old > need
-    int need = S - recent;
-    uint32_t prefix = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int j = tid; j < old; j += kSeedThreads) {
-            const uint32_t key = weight_key(w[j]);
-            if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
-        }
-        __syncthreads();
-        if (warp == 0) {  // the digit at which the count from above reaches need
-            int own[8], sum = 0;  // lane: digits 255 - 8 lane - i
+    sync();  // every CTA's positions are visible; no CTA reads another's shared memory after this
+    const __nv_bfloat16* kb = k + b * ksb + h * ksh;
+    const __nv_bfloat16* vb = v + b * vsb + h * vsh;
+    const int rows = kSeedThreads / vpr, e = tid % vpr;  // rows of a step; this thread's 16 bytes of a row
+    const int kept = min(n, S), part = (kept + C - 1) / C;
+    const int s1 = min(kept, (rank + 1) * part);
+    constexpr int kUnroll = 4;
+    for (int s0 = rank * part + tid / vpr; s0 < s1; s0 += kUnroll * rows) {
+        uint4 x[kUnroll], y[kUnroll];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += own[i] = hist[255 - 8 * lane - i];
-            int incl = sum;
+        for (int u = 0; u < kUnroll; ++u) {
+            const int s = s0 + u * rows;
+            if (s >= s1) continue;
+            const int64_t j = __ldcg(po + s);
+            x[u] = ld_stream_16(kb + j * kst + 8 * e);
+            y[u] = ld_stream_16(vb + j * vst + 8 * e);
+        }
 #pragma unroll
-            for (int x = 1; x < 32; x <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, incl, x);
-                if (lane >= x) incl += y;
-            }
-            int before = incl - sum;
-            if (before < need && need <= incl) {
-                int i = 0;
-                while (before + own[i] < need) before += own[i++];
-                sm_prefix = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
-                sm_need = need - before;
-            }
+        for (int u = 0; u < kUnroll; ++u) {
+            const int s = s0 + u * rows;
+            if (s >= s1) continue;
+            kc[(bh * S + s) * vpr + e] = x[u];
+            vc[(bh * S + s) * vpr + e] = y[u];
         }
-        __syncthreads();
-        prefix = sm_prefix;
-        need = sm_need;
-        __syncthreads();
-    }
-    // Keep keys > prefix and the first `need` keys equal to it. Each warp takes one run of
-    // positions; the counts of the warps before it say where its own go.
-    const int run = ((old + 31) / 32 + 31) / 32 * 32;
-    const int j0 = min(old, warp * run), j1 = min(old, j0 + run);
-    int above = 0, equal = 0;
-    for (int j = j0 + lane; j - lane < j1; j += 32) {
-        const uint32_t key = j < j1 ? weight_key(w[j]) : 0u;
-        above += __popc(__ballot_sync(0xffffffffu, j < j1 && key > prefix));
-        equal += __popc(__ballot_sync(0xffffffffu, j < j1 && key == prefix));
-    }
-    if (lane == 0) {
-        sm_a[warp] = above;
-        sm_b[warp] = equal;
-    }
-    __syncthreads();
-    int na = 0, ne = 0;  // kept above and seen equal before this position
-    for (int x = 0; x < warp; ++x) {
-        na += sm_a[x];
-        ne += sm_b[x];
-    }
-    const uint32_t below = (1u << lane) - 1u;
-    for (int j = j0 + lane; j - lane < j1; j += 32) {
-        const float x = j < j1 ? w[j] : 0.f;
-        const uint32_t key = weight_key(x);
-        const uint32_t ba = __ballot_sync(0xffffffffu, j < j1 && key > prefix);
-        const uint32_t be = __ballot_sync(0xffffffffu, j < j1 && key == prefix);
-        const int a = na + __popc(ba & below), e = ne + __popc(be & below);
-        const bool take = j < j1 && (key > prefix || (key == prefix && e < need));
-        if (take) {
-            const int at = a + min(e, need);
-            wo[at] = x;
-            po[at] = j;
-        }
-        na += __popc(ba);
-        ne += __popc(be);
-    }
-    for (int i = tid; i < recent; i += kSeedThreads) {
-        wo[S - recent + i] = w[old + i];
-        po[S - recent + i] = old + i;
-    }
-}
-
-// Copy the kept positions' key and value rows into their slots, 16 bytes a thread.
-__global__ void __launch_bounds__(256)
-    seed_gather_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
-                       const int64_t* __restrict__ lens, const int64_t* __restrict__ pc, uint4* __restrict__ kc,
-                       uint4* __restrict__ vc, int64_t ksb, int64_t ksh, int64_t kst, int64_t vsb, int64_t vsh,
-                       int64_t vst, int Hkv, int T, int S, int vpr, int64_t n_vec) {
-    ptx::grid_dependency_wait();
-    for (int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < n_vec; x += (int64_t)gridDim.x * blockDim.x) {
-        const int e = (int)(x % vpr);
-        const int64_t row = x / vpr;  // bh * S + slot
-        const int64_t bh = row / S, b = bh / Hkv, h = bh - b * Hkv;
-        const int64_t n = lens == nullptr ? T : lens[b];
-        if (n < 0 || n > T || row - bh * S >= n) continue;
-        const int64_t j = pc[row];
-        kc[x] = *reinterpret_cast<const uint4*>(k + b * ksb + h * ksh + j * kst + 8 * e);
-        vc[x] = *reinterpret_cast<const uint4*>(v + b * vsb + h * vsh + j * vst + 8 * e);
     }
 }
 

@@ -175,14 +175,16 @@ void split(int64_t units, int64_t keys, int* n, int* chunk) {
 // Key tiles that a CTA of prefix_kernel takes, of `tiles`, when `groups` CTAs take them all: the
 // fewest rounds of 148 CTAs (one fits an SM) by the length of a round, where the start and end
 // of a CTA count as 3 tiles and a further partial state to join as half a tile.
-int64_t prefix_chunk(int64_t groups, int64_t tiles, int64_t least) {
-    int64_t best = tiles, cost = INT64_MAX;
-    for (int64_t ns = 1; ns <= tiles && ns <= 148; ++ns) {
-        int64_t chunk = (tiles + ns - 1) / ns;
+int prefix_chunk(int64_t groups, int tiles, int least) {
+    int best = tiles;
+    int64_t cost = INT64_MAX;
+    for (int ns = 1; ns <= tiles && (ns == 1 || groups * ns <= 2 * 148); ++ns) {
+        int chunk = (tiles + ns - 1) / ns;
         if (chunk < least) chunk = least;
-        const int64_t splits = (tiles + chunk - 1) / chunk, rounds = (groups * splits + 147) / 148;
-        if (rounds * 2 * (chunk + 3) + splits < cost) {
-            cost = rounds * 2 * (chunk + 3) + splits;
+        const int splits = (tiles + chunk - 1) / chunk;
+        const int64_t c = (groups * splits + 147) / 148 * 2 * (chunk + 3) + splits;
+        if (c < cost) {
+            cost = c;
             best = chunk;
         }
     }
@@ -234,9 +236,10 @@ Plan plan(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D, bo
     int64_t prefix_ctas = 0;
     if (P > p.P0) {
         p.pair = B * G > 128;
-        const int64_t tiles = (P + 127) / 128, groups = Hkv * (p.pair ? (B * G + 255) / 256 : 1);
-        p.pchunk = (int)prefix_chunk(groups, tiles, p.pair ? 1 : 2);
-        p.np = (int)((tiles + p.pchunk - 1) / p.pchunk);
+        const int tiles = (int)((P + 127) / 128);
+        const int64_t groups = Hkv * (p.pair ? (B * G + 255) / 256 : 1);
+        p.pchunk = prefix_chunk(groups, tiles, p.pair ? 1 : 2);
+        p.np = (tiles + p.pchunk - 1) / p.pchunk;
         prefix_ctas = groups * p.np;
     }
     // Beside the prefix's kernel when that leaves half of the SMs free (24 streams of 32 heads, 4 to a
@@ -248,7 +251,6 @@ Plan plan(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D, bo
     p.off_o = round256(B * H * p.NS * 8);
     p.off_scores = p.off_o + round256(B * H * p.NS * D * 4);
     p.bytes = p.off_scores + (scores && p.C == 0 ? round256(B * H * S * 4) : 0);
-    if (p.bytes < 256) p.bytes = 256;
     return p;
 }
 
@@ -339,9 +341,10 @@ int decode(const char* fn, const void* q, const void* k, const void* v, const in
     if (!std::isfinite(scale)) return fail(SWA_ERR_INVALID_ARG, "%s: scale must be finite", fn);
     if (B == 0 || H == 0) return success();
     if (!(scale > 0.0)) return fail(SWA_ERR_UNSUPPORTED, "%s: scale must be > 0 (got %g)", fn, scale);
-    if (!q || !k || !v || !pos || !out || !workspace || (scores && !weights) || (P > 0 && (!kp || !vp)))
+    if (!q || !k || !v || !pos || !out || (scores && !weights) || (P > 0 && (!kp || !vp)))
         return fail(SWA_ERR_INVALID_ARG, "%s: null pointer", fn);
     const Plan pl = plan(B, H, Hkv, S, P, D, scores);
+    if (pl.bytes > 0 && !workspace) return fail(SWA_ERR_INVALID_ARG, "%s: null workspace", fn);
     if (workspace_bytes < pl.bytes)
         return fail(SWA_ERR_INVALID_ARG, "%s: workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes,
                     (long long)pl.bytes);
@@ -475,7 +478,8 @@ int swa_cache_seed(const void* k, const void* v, const float* weights, const int
     if (!k || !v || !weights || !kcache || !vcache || !wcache || !pcache)
         return fail(SWA_ERR_INVALID_ARG, "%s: null pointer", fn);
     if (int rc = check_head_dim(fn, D)) return rc;
-    if (T > INT32_MAX / 2 || S > INT32_MAX / 2) return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    if (T > INT32_MAX / 2 || S > INT32_MAX / 2 || B * Hkv > INT32_MAX / 8)
+        return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kcache, 16) || !aligned(vcache, 16))
         return fail(SWA_ERR_MISALIGNED, "%s: key and value tensors must be 16-byte aligned", fn);
     if (!aligned(weights, 4) || !aligned(wcache, 4) || !aligned(pcache, 8) || !aligned(lens, 8))
@@ -486,17 +490,21 @@ int swa_cache_seed(const void* k, const void* v, const float* weights, const int
     int *status, num_sms;
     if (int rc = swa_internal::device_info(&status, &num_sms)) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    swa::seed_select_kernel<<<(unsigned)(B * Hkv), swa::kSeedThreads, 0, s>>>(weights, lens, wcache, pcache, (int)Hkv,
-                                                                             (int)T, (int)S, (int)recent, status);
-    if (int rc = launched(fn)) return rc;
-    const int vpr = (int)(D / 8);
-    const int64_t n_vec = B * Hkv * S * vpr;
-    int64_t blocks = (n_vec + 255) / 256;
-    if (blocks > 148 * 32) blocks = 148 * 32;
-    launch_after(dim3((unsigned)blocks), 256, 0, s, swa::seed_gather_kernel, static_cast<const __nv_bfloat16*>(k),
-                 static_cast<const __nv_bfloat16*>(v), lens, static_cast<const int64_t*>(pcache),
-                 static_cast<uint4*>(kcache), static_cast<uint4*>(vcache), st[0], st[1], st[2], st[3], st[4], st[5],
-                 (int)Hkv, (int)T, (int)S, vpr, n_vec);
+    // A cluster while the heads alone do not fill the SMs, each CTA keeping a step's worth of
+    // positions.
+    int C = 1;
+    while (C < 8 && B * Hkv * C < 148 && T >= 2 * C * swa::kSeedThreads) C *= 2;
+    cudaLaunchConfig_t cfg = config(dim3((unsigned)(B * Hkv * C)), swa::kSeedThreads, 0, s);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)C;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    cudaLaunchKernelEx(&cfg, swa::cache_seed_kernel, static_cast<const __nv_bfloat16*>(k),
+                       static_cast<const __nv_bfloat16*>(v), weights, lens, static_cast<uint4*>(kcache),
+                       static_cast<uint4*>(vcache), wcache, pcache, st[0], st[1], st[2], st[3], st[4], st[5], (int)Hkv,
+                       (int)T, (int)S, (int)recent, (int)(D / 8), C, status);
     if (int rc = launched(fn)) return rc;
     return success();
 }
@@ -521,7 +529,7 @@ int swa_cache_append(const void* k, const void* v, void* kcache, void* vcache, f
     int *status, num_sms;
     if (int rc = swa_internal::device_info(&status, &num_sms)) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    swa::cache_append_kernel<<<(unsigned)(B * Hkv), 256, 0, s>>>(
+    swa::cache_append_kernel<<<(unsigned)(B * Hkv), swa::kAppendThreads, 0, s>>>(
         static_cast<const uint4*>(k), static_cast<const uint4*>(v), static_cast<uint4*>(kcache),
         static_cast<uint4*>(vcache), wcache, pcache, pos, slots, (int)Hkv, (int)S, (int)recent, (int)(D / 8), status);
     if (int rc = launched(fn)) return rc;

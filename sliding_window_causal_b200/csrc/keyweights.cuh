@@ -400,25 +400,25 @@ __global__ void __launch_bounds__(kKwThreads, 2)
     // the sums of the two warpgroups, then of the cluster's CTAs, in that order
     if (warp >= 2) sm_red[128 * ((warp - 2) >> 2) + 32 * (warp & 3) + lane] = sum;
     if (C > 1) {
-        asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+        ptx::cluster_arrive();
+        ptx::cluster_wait();
     } else {
         __syncthreads();
     }
     if (rank == 0 && tid < 128) {
         float w = sm_red[tid] + sm_red[128 + tid];
         for (int r = 1; r < C; ++r) {
-            float x, z;
-            uint32_t from;
-            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(ptx::smem_u32(sm_red + tid)), "r"(r));
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(from));
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(z) : "r"(from + 512));
-            w += x + z;
+            const uint32_t from = ptx::cluster_addr(sm_red + tid, r);
+            w += ptx::cluster_ld(from) + ptx::cluster_ld(from + 512);
         }
         const int j = it.j0 + tid;
         // a key past the stream's end may have met anything in its row
         if (j < T) out[(it.b * Hkv + it.hk) * T + j] = j < it.n ? w : 0.f;
     }
-    if (C > 1) asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    if (C > 1) {  // the other CTAs' sums are read before they leave
+        ptx::cluster_arrive();
+        ptx::cluster_wait();
+    }
 }
 
 }  // namespace swa

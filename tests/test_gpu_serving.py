@@ -404,7 +404,7 @@ def test_decode_offsets_past_32_bits():
 
 
 def test_decode_workspace_and_out_of_the_caller():
-    B, H, Hkv, D, S, P = 3, 4, 2, 64, 70, 90
+    B, H, Hkv, D, S, P = 3, 18, 2, 64, 70, 90
     g = gen(36)
     q, kc, vc, kp, vp = rand(g, B, H, D), rand(g, B, Hkv, S, D), rand(g, B, Hkv, S, D), rand(g, Hkv, P, D), rand(g, Hkv, P, D)
     pos = torch.tensor([3, 69, 500], device=DEV)

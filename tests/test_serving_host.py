@@ -75,7 +75,7 @@ def test_cache_append_refusals(lib):
 
 
 def test_decode_refusals(lib):
-    size = dict(B=2, H=4, Hkv=2, S=5, P=3, D=64)
+    size = dict(B=2, H=38, Hkv=2, S=5, P=3, D=64)  # more than 8 query heads to a key head: a workspace
     for fn, need in ((lib.swa_cache_decode, lib.swa_cache_decode_workspace_bytes),
                      (lib.swa_prefix_decode, lib.swa_prefix_decode_workspace_bytes)):
         ws = need(*size.values())
@@ -97,6 +97,8 @@ def test_decode_refusals(lib):
                     dict(pos=P0 + 4), dict(st=strides(192, 68, 192, 64))):
             assert f(**bad) == MISALIGNED, bad
         assert f(B=0) == OK and f(H=0) == OK
+        assert need(2, 4, 2, 5, 3, 64) == 0  # one cluster a key head needs none
+        assert f(H=4, ws=None, nbytes=0, q=None) == INVALID
         assert need(2, 4, 3, 5, 3, 64) == -1 and need(2, 4, 2, 0, 3, 64) == -1 and need(2, 4, 2, 5, 3, 80) == -1
         assert need(0, 4, 2, 5, 3, 64) == 0
     assert lib.swa_cache_decode(P0, P0, P0, P0 + 2, P0, None, None, P0, P0, 1 << 30, 2, 4, 2, 5, 0, 64, 0.125, None,
