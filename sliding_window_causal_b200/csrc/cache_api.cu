@@ -85,6 +85,14 @@ cudaLaunchConfig_t config(dim3 grid, unsigned block, size_t smem, cudaStream_t s
     c.stream = s;
     return c;
 }
+// Clusters of C CTAs along x; at: the launch's one attribute.
+void cluster_of(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* at, int C) {
+    at->id = cudaLaunchAttributeClusterDimension;
+    at->val.clusterDim.x = (unsigned)C;
+    at->val.clusterDim.y = at->val.clusterDim.z = 1;
+    cfg->attrs = at;
+    cfg->numAttrs = C > 1 ? 1 : 0;
+}
 // A launch that may start before the kernel ahead of it on the stream has ended; the kernel
 // itself waits (grid_dependency_wait).
 template <typename... P, typename... A>
@@ -135,17 +143,14 @@ int launch_key_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const f
     const int64_t slices = H / Hkv * ((rows + swa::kKwSlice - 1) / swa::kKwSlice);
     int C = 1;
     while (C < 8 && work * C < 2 * 148 && slices >= 8 * C) C *= 2;
-    const int64_t grid = B * Hkv * tiles * C;
-    if (grid > INT32_MAX) C = 1;
-    cudaLaunchConfig_t cfg = config(dim3((unsigned)(B * Hkv * tiles * C)), swa::kKwThreads, swa::KwCfg<D>::kSmemBytes, s);
+    const int64_t units = B * Hkv * tiles;
+    if (units * C > INT32_MAX) C = 1;
+    const int64_t grid = C > 1 ? units * C : units < 2 * 148 ? units : 2 * 148;
+    cudaLaunchConfig_t cfg = config(dim3((unsigned)grid), swa::kKwThreads, swa::KwCfg<D>::kSmemBytes, s);
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)C;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = C > 1 ? 1 : 0;
-    cudaLaunchKernelEx(&cfg, kernel, tm_q, tm_k, lse, lens, weights, (int)H, (int)Hkv, (int)T, W, last,
-                       (float)(1.4426950408889634 * scale), C, swa_internal::wait_limit_ns(), status);
+    cluster_of(&cfg, at, C);
+    cudaLaunchKernelEx(&cfg, kernel, tm_q, tm_k, lse, lens, weights, units, (int)H, (int)Hkv, (int)T, W,
+                       last, (float)(1.4426950408889634 * scale), C, swa_internal::wait_limit_ns(), status);
     return SWA_OK;
 }
 
@@ -457,9 +462,16 @@ int swa_key_weights(const void* q, const void* k, const float* lse, const int64_
                               : launch_key_weights<64>(tm_q, tm_k, lse, lens, weights, B, H, Hkv, T, Wi, Li, scale, status, s))
             return rc;
     } else {
-        swa::key_weights_simt_kernel<<<(unsigned)(B * Hkv * n_kt), 256, 0, s>>>(
-            static_cast<const float*>(q), static_cast<const float*>(k), lse, lens, weights, qs[0], qs[1], qs[2], ks[0],
-            ks[1], ks[2], (int)H, (int)Hkv, (int)T, (int)D, Wi, Li, (float)scale, (int)n_kt, status);
+        // a cluster splits the query tiles while the CTAs do not fill the SMs twice
+        const int64_t units = B * Hkv * n_kt, tiles = H / Hkv * ((swa::kKwTile + (Wi < Li ? Wi : Li) + 62) / swa::kKwTile);
+        int C = 1;
+        while (C < 8 && units * C < 2 * 148 && tiles >= 2 * C) C *= 2;
+        cudaLaunchConfig_t cfg = config(dim3((unsigned)(units * C)), swa::kKwSimtThreads, 0, s);
+        cudaLaunchAttribute at[1];
+        cluster_of(&cfg, at, C);
+        cudaLaunchKernelEx(&cfg, swa::key_weights_simt_kernel, static_cast<const float*>(q), static_cast<const float*>(k),
+                           lse, lens, weights, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], (int)H, (int)Hkv, (int)T, (int)D,
+                           Wi, Li, (float)scale, (int)n_kt, C, status);
     }
     if (int rc = launched(fn)) return rc;
     return success();
@@ -496,11 +508,7 @@ int swa_cache_seed(const void* k, const void* v, const float* weights, const int
     while (C < 8 && B * Hkv * C < 148 && T >= 2 * C * swa::kSeedThreads) C *= 2;
     cudaLaunchConfig_t cfg = config(dim3((unsigned)(B * Hkv * C)), swa::kSeedThreads, 0, s);
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)C;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = C > 1 ? 1 : 0;
+    cluster_of(&cfg, at, C);
     cudaLaunchKernelEx(&cfg, swa::cache_seed_kernel, static_cast<const __nv_bfloat16*>(k),
                        static_cast<const __nv_bfloat16*>(v), weights, lens, static_cast<uint4*>(kcache),
                        static_cast<uint4*>(vcache), wcache, pcache, st[0], st[1], st[2], st[3], st[4], st[5], (int)Hkv,
