@@ -366,6 +366,8 @@ int swa_decode_noalloc(const void* q, const void* kring, const void* vring, cons
  * numbers: -0 equals 0, NaN counts as +infinity, ties go to the lowest slot (or position).
  * Usual order: swa_forward_lse on the prompt, swa_key_weights, swa_cache_seed; then for each
  * token swa_cache_append and swa_cache_decode.
+ * The calls allocate nothing and can be captured into a graph; the first call on a device of
+ * each kind sets kernel attributes and is made before any capture.
  */
 
 /*

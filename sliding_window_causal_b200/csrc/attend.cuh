@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
 }
 // The slots that the query at position P sees: none, and a report, if it is negative.
 __device__ __forceinline__ int attend_slots(int64_t P, int S, int* status, bool report) {
-    if (P >= 0) return (int)(P + 1 < (int64_t)S ? P + 1 : (int64_t)S);
+    if (P >= 0) return P < (int64_t)S ? (int)P + 1 : S;
     if (report) atomicCAS(status, 0, kStatusInvalid);
     return 0;
 }
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kFinishThreads)
     const int s0 = (int)(x % slot_blocks) * kFinishSlots;
     const int64_t b = unit / a.Hkv;
     const int64_t P = a.pos[b];
-    const int n = P < 0 ? 0 : (int)(P + 1 < (int64_t)a.S ? P + 1 : (int64_t)a.S);
+    const int n = attend_slots(P, a.S, a.status, false);
     if (s0 >= n) return;
     const int64_t row0 = b * a.H + (unit % a.Hkv) * a.G;
     for (int h = warp; h < a.G; h += 4) {

@@ -9,8 +9,6 @@
 #include <cstdint>
 #include <cstdio>
 #include <mutex>
-#include <set>
-#include <utility>
 
 #include "api_internal.h"
 #include "attend.cuh"
@@ -109,13 +107,20 @@ void launch_after(dim3 grid, unsigned block, size_t smem, cudaStream_t s, void (
 // Let `kernel` use `bytes` of dynamic shared memory on the current device, and check that it was
 // compiled with `regs` registers a thread if that is given (once a device).
 int allow_smem(const void* kernel, int bytes, int regs = 0) {
+    struct Done {
+        int dev;
+        const void* kernel;
+    };
+    constexpr int kMost = 256;  // more (device, kernel) pairs than that are set again each time
     static std::mutex mu;
-    static std::set<std::pair<int, const void*>> done;
+    static Done done[kMost];
+    static int n_done = 0;
     int dev;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return fail(SWA_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
     std::lock_guard<std::mutex> lk(mu);
-    if (done.count({dev, kernel})) return SWA_OK;
+    for (int i = 0; i < n_done; ++i)
+        if (done[i].dev == dev && done[i].kernel == kernel) return SWA_OK;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return fail(SWA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     cudaFuncAttributes at;
@@ -123,7 +128,7 @@ int allow_smem(const void* kernel, int bytes, int regs = 0) {
     if (e != cudaSuccess) return fail(SWA_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
     if (regs > 0 && at.numRegs != regs)
         return fail(SWA_ERR_CUDA, "a kernel was compiled with %d registers a thread, %d expected", at.numRegs, regs);
-    done.insert({dev, kernel});
+    if (n_done < kMost) done[n_done++] = {dev, kernel};
     return SWA_OK;
 }
 

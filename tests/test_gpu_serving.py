@@ -60,6 +60,9 @@ KEY_CASES = [
     (1, 2, 1, 1500, 64, 1500, 64, False, BF),
     (2, 1, 2, 1111, 128, 257, 300, True, BF),
     (1, 1, 1, 4100, 128, 4096, None, False, BF),
+    (4, 8, 1, 1300, 64, 40, None, True, BF),       # more key tiles than CTAs
+    (6, 8, 1, 1000, 128, 130, 20, True, BF),       # most of them seen by no counted query
+    (7, 7, 1, 900, 128, 300, 1, True, BF),         # one slice a tile
     (1, 1, 1, 1, 1, 1, None, False, torch.float32),
     (2, 2, 2, 70, 40, 9, None, True, torch.float32),
     (1, 1, 1, 333, 80, 100, 50, False, torch.float32),
@@ -297,6 +300,9 @@ DECODE_CASES = [
     (24, 1, 4, 128, 333, 2000), (33, 2, 1, 64, 40, 777), (130, 1, 1, 128, 3, 257), (64, 1, 5, 64, 20, 4100),
     (2, 1, 1, 128, 5000, 9), (100, 2, 8, 128, 9, 1500), (1, 1, 70, 64, 129, 128), (16, 1, 1, 128, 64, 128),
     (32, 2, 8, 64, 31, 640),
+    # prefixes too long for each stream to read by itself
+    (24, 2, 4, 128, 50, 1100), (60, 2, 2, 64, 70, 2100), (100, 2, 3, 64, 33, 700), (16, 1, 8, 128, 40, 4000),
+    (2, 1, 1, 128, 30, 140000), (3, 2, 12, 64, 500, 5000), (9, 1, 1, 64, 100, 40001), (40, 8, 1, 128, 600, 300),
 ]
 
 
@@ -335,10 +341,10 @@ def test_decode_never_reads_slots_without_a_token(G):
     swa.device_status()
 
 
-@pytest.mark.parametrize("B,G", [(2, 1), (40, 4)])
-def test_decode_reads_a_strided_prefix_and_nothing_past_it(B, G):
+@pytest.mark.parametrize("B,G,P", [(2, 1, 200), (40, 4, 200), (40, 4, 1000), (20, 4, 2000)])
+def test_decode_reads_a_strided_prefix_and_nothing_past_it(B, G, P):
     """A prefix that is a slice of a longer [P,Hkv,D] buffer whose other rows hold NaN."""
-    Hkv, D, S, P = 3, 64, 20, 200
+    Hkv, D, S = 3, 64, 20
     g = gen(32)
     q, kc, vc = rand(g, B, Hkv * G, D), rand(g, B, Hkv, S, D), rand(g, B, Hkv, S, D)
     buf = torch.full((2, P + 90, Hkv, D), math.nan, dtype=BF, device=DEV)
@@ -349,7 +355,7 @@ def test_decode_reads_a_strided_prefix_and_nothing_past_it(B, G):
     assert torch.equal(out, swa.prefix_decode(q, kp.contiguous(), vp.contiguous(), kc, vc, pos, S))
 
 
-@pytest.mark.parametrize("B,G,P", [(1, 1, 300), (3, 8, 500), (80, 2, 700)])
+@pytest.mark.parametrize("B,G,P", [(1, 1, 300), (3, 8, 500), (80, 2, 700), (80, 2, 2000), (40, 2, 4000)])
 def test_decode_of_sharp_and_growing_scores(B, G, P):
     """Scores that grow along the keys by hundreds, so that every running maximum is replaced
     many times, and rows where one key far outweighs the rest."""
@@ -382,6 +388,32 @@ def test_decode_reports_a_negative_position():
         assert e.value.code == 1
         assert bool((out[1] == 0).all()) and torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
         assert torch.equal(w[1], wc[1])
+
+
+def test_decode_of_the_last_position():
+    B, H, D, S = 2, 2, 64, 33
+    g = gen(37)
+    q, kc, vc = rand(g, B, H, D), rand(g, B, H, S, D), rand(g, B, H, S, D)
+    far = torch.full((B,), torch.iinfo(torch.int64).max, device=DEV)
+    assert torch.equal(swa.prefix_decode(q, None, None, kc, vc, far, S),
+                       swa.prefix_decode(q, None, None, kc, vc, torch.full_like(far, S), S))
+    swa.device_status()
+
+
+def test_decode_of_broadcast_prefix_heads():
+    """A prefix whose key heads are one head, expanded (stride 0), and an expanded prompt."""
+    B, Hkv, G, D, S, P = 40, 4, 2, 64, 10, 3000
+    g = gen(38)
+    q, kc, vc = rand(g, B, Hkv * G, D), rand(g, B, Hkv, S, D), rand(g, B, Hkv, S, D)
+    kp, vp = (rand(g, 1, P, D).expand(Hkv, P, D) for _ in range(2))
+    pos = torch.full((B,), 20, device=DEV)
+    a = check_decode(q, kc, vc, pos, kp, vp)
+    assert torch.equal(a, swa.prefix_decode(q, kp.contiguous(), vp.contiguous(), kc, vc, pos, S))
+    k = rand(g, 1, 1, 300, D).expand(2, 3, 300, D)
+    qq = rand(g, 2, 6, 300, D)
+    lse = band_lse(qq, k, 50)
+    assert torch.equal(swa.key_weights(qq, k, lse, 50), swa.key_weights(qq, k.contiguous(), lse, 50))
+    swa.device_status()
 
 
 def test_decode_offsets_past_32_bits():
@@ -456,10 +488,11 @@ def test_serving_a_prompt_and_its_tokens():
     serve(2, 1, 1, 128, 300, 129, 0, 300, 130, 6, 42)
 
 
-def test_captured_steps_replay():
+@pytest.mark.parametrize("P", [300, 5000])
+def test_captured_steps_replay(P):
     """append + decode captured into a graph: two graphs of their own workspaces, replayed in
     turn on other data, give what plain calls give."""
-    B, H, Hkv, D, S, P, recent = 6, 4, 2, 128, 50, 300, 9
+    B, H, Hkv, D, S, recent = 6, 4, 2, 128, 50, 9
     g = gen(51)
     kp, vp = rand(g, Hkv, P, D), rand(g, Hkv, P, D)
 
@@ -502,9 +535,10 @@ def test_captured_steps_replay():
     swa.device_status()
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("P", [900, 9000])
+def test_two_streams_at_once(P):
     """Calls on two streams with workspaces of their own, interleaved, equal calls alone."""
-    B, H, D, S, P = 4, 8, 64, 700, 900
+    B, H, D, S = 12, 8, 64, 700
     g = gen(61)
     sets = [(rand(g, B, H, D), rand(g, 8, P, D), rand(g, 8, P, D), rand(g, B, 8, S, D), rand(g, B, 8, S, D),
              torch.randint(0, 2000, (B,), generator=g, device=DEV)) for _ in range(2)]
