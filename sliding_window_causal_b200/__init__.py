@@ -34,6 +34,7 @@ shares, and a cache of a fixed budget that forgets by attention weight instead o
                                         decode over the cache, whose weights it updates
 """
 import ctypes
+import functools
 
 from . import _native
 from ._native import SWA_BF16, SWA_F32, SwaError, check
@@ -46,6 +47,7 @@ __all__ = ["forward", "forward_lse", "backward", "band_weights", "decode", "chun
            "prefix_decode_workspace_bytes", "cache_decode_workspace_bytes", "SwaError"]
 
 
+@functools.lru_cache(maxsize=None)
 def _torch():
     import torch
     return torch
@@ -348,7 +350,7 @@ def _same_device(dense, strided=()):
     a contiguous head dimension."""
     d = dense[0].get_device()
     for t in dense:
-        if t.get_device() != d or d < 0 or not t.is_contiguous():
+        if d < 0 or t.get_device() != d or not t.is_contiguous():
             _need_cuda(dense[0], t)  # says what is wrong
     for t in strided:
         if t.get_device() != d:
@@ -361,11 +363,21 @@ def _same_device(dense, strided=()):
 def _launch(index, fn, *args):
     """fn(*args, current stream) with device `index` as the current one."""
     torch = _torch()
-    if index == torch.cuda.current_device():
-        check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        check(rc)
+
+
+@functools.lru_cache(maxsize=4096)
+def _decode_workspace(weighted, B, H, Hkv, S, P, D):
+    """Bytes of workspace of a decode of these sizes; they alone decide it."""
+    lib = _native.lib()
+    fn = lib.swa_cache_decode_workspace_bytes if weighted else lib.swa_prefix_decode_workspace_bytes
+    return int(fn(B, H, Hkv, S, P, D))
 
 
 def _heads(H, Hkv):
@@ -400,7 +412,7 @@ def key_weights(q, k, lse, window, lens=None, last=None, scale=None):
     if lens is not None:
         _positions(lens, B, "lens")
     dev = _same_device((lse,) if lens is None else (lse, lens), (q, k))
-    out = torch.empty((B, Hkv, T), dtype=torch.float32, device=q.device)
+    out = lse.new_empty((B, Hkv, T))
     sc = 1.0 / D ** 0.5 if scale is None else float(scale)
     strides = None if q.is_contiguous() and k.is_contiguous() else _bht_strides(q, k)
     _launch(dev, _native.lib().swa_key_weights, q.data_ptr(), k.data_ptr(), lse.data_ptr(),
@@ -415,11 +427,13 @@ def _budget_cache(kcache, vcache, wcache, pcache):
     shape = kcache.shape
     if len(shape) != 4 or vcache.shape != shape:
         raise ValueError("kcache and vcache must share one [B,Hkv,S,D] shape")
-    if kcache.dtype != torch.bfloat16 or vcache.dtype != torch.bfloat16:
+    bf16 = torch.bfloat16
+    if kcache.dtype != bf16 or vcache.dtype != bf16:
         raise TypeError("the cache's keys and values are bf16")
-    if wcache.dtype != torch.float32 or wcache.shape != shape[:3]:
+    slots = shape[:3]
+    if wcache.dtype != torch.float32 or wcache.shape != slots:
         raise ValueError("wcache must be fp32 [B,Hkv,S]")
-    if pcache is not None and (pcache.dtype != torch.int64 or pcache.shape != shape[:3]):
+    if pcache is not None and (pcache.dtype != torch.int64 or pcache.shape != slots):
         raise ValueError("pcache must be int64 [B,Hkv,S]")
     return shape
 
@@ -459,71 +473,75 @@ def cache_append(k, v, kcache, vcache, wcache, pcache, pos, recent):
     at 0. Returns the slots taken, [B,Hkv] int64."""
     torch = _torch()
     B, Hkv, S, D = _budget_cache(kcache, vcache, wcache, pcache)
-    if k.shape != (B, Hkv, D) or v.shape != k.shape:
+    shape = k.shape
+    if shape != (B, Hkv, D) or v.shape != shape:
         raise ValueError("k and v must be [B,Hkv,D]")
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
         raise TypeError("the cache's keys and values are bf16")
     _positions(pos, B)
     dev = _same_device((k, v, kcache, vcache, wcache, pcache, pos))
-    slots = torch.empty((B, Hkv), dtype=torch.int64, device=k.device)
+    slots = pos.new_empty((B, Hkv))
     _launch(dev, _native.lib().swa_cache_append, k.data_ptr(), v.data_ptr(), kcache.data_ptr(), vcache.data_ptr(),
             wcache.data_ptr(), pcache.data_ptr(), pos.data_ptr(), slots.data_ptr(), B, Hkv, D, S, int(recent))
     return slots
 
 
-def _decode(fn, need, weighted, q, kc, vc, wc, pos, kprefix, vprefix, S, Hkv, out, scale, workspace):
+def _decode(fn, weighted, q, kc, vc, wc, pos, kprefix, vprefix, S, Hkv, out, scale, workspace):
     """The two decodes' common part: prefix, buffers and call."""
     torch = _torch()
-    B, H, D = q.shape
+    B, H, D = shape = q.shape
     _heads(H, Hkv)
     _positions(pos, B)
-    if (kprefix is None) != (vprefix is None):
-        raise ValueError("give both kprefix and vprefix, or neither")
     dense = [q, kc, vc, pos]
     if weighted:
         dense.append(wc)
     P, kp, vp, strides, prefix = 0, None, None, None, ()
-    if kprefix is not None:
-        if kprefix.dim() != 3 or vprefix.shape != kprefix.shape or (kprefix.shape[0], kprefix.shape[2]) != (Hkv, D):
+    if kprefix is not None and vprefix is not None:
+        pshape = kprefix.shape
+        if len(pshape) != 3 or vprefix.shape != pshape or pshape[0] != Hkv or pshape[2] != D:
             raise ValueError("kprefix and vprefix must share one [Hkv,P,D] shape")
         if kprefix.dtype != torch.bfloat16 or vprefix.dtype != torch.bfloat16:
             raise TypeError("the prefix is bf16")
-        P = kprefix.shape[1]
+        P = pshape[1]
         if P:
-            prefix = (kprefix, vprefix)
             kp, vp = kprefix.data_ptr(), vprefix.data_ptr()
-            if not (kprefix.is_contiguous() and vprefix.is_contiguous()):
+            if kprefix.is_contiguous() and vprefix.is_contiguous():
+                dense += (kprefix, vprefix)
+            else:
+                prefix = (kprefix, vprefix)
                 strides = (ctypes.c_int64 * 4)(*kprefix.stride()[:2], *vprefix.stride()[:2])
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    else:
-        if out.shape != q.shape or out.dtype != q.dtype:
+    elif kprefix is not None or vprefix is not None:
+        raise ValueError("give both kprefix and vprefix, or neither")
+    if out is not None:
+        if out.shape != shape or out.dtype != q.dtype:
             raise ValueError("out must match q")
         dense.append(out)
     if workspace is not None:
         dense.append(workspace)
     dev = _same_device(dense, prefix)
+    if out is None:
+        out = torch.empty_like(q)
     ws, have = None, 0
     if workspace is not None:
         ws, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     else:
-        have = need(B, H, Hkv, S, P, D)
+        have = _decode_workspace(weighted, B, H, Hkv, S, P, D)
         if have > 0:
             workspace = torch.empty(have, dtype=torch.uint8, device=q.device)
             ws = workspace.data_ptr()
     sc = 1.0 / D ** 0.5 if scale is None else float(scale)
-    cache = (kc.data_ptr(), vc.data_ptr())
     if weighted:
-        args = (q.data_ptr(), *cache, wc.data_ptr(), pos.data_ptr(), kp, vp)
+        _launch(dev, fn, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), wc.data_ptr(), pos.data_ptr(), kp, vp,
+                out.data_ptr(), ws, have, B, H, Hkv, S, P, D, sc, strides)
     else:
-        args = (q.data_ptr(), kp, vp, *cache, pos.data_ptr())
-    _launch(dev, fn, *args, out.data_ptr(), ws, have, B, H, Hkv, S, P, D, sc, strides)
+        _launch(dev, fn, q.data_ptr(), kp, vp, kc.data_ptr(), vc.data_ptr(), pos.data_ptr(), out.data_ptr(), ws, have,
+                B, H, Hkv, S, P, D, sc, strides)
     return out
 
 
 def cache_decode_workspace_bytes(B, H, Hkv, S, P, D):
     """Bytes of device workspace cache_decode needs (0: none)."""
-    return int(_native.lib().swa_cache_decode_workspace_bytes(B, H, Hkv, S, P, D))
+    return _decode_workspace(True, B, H, Hkv, S, P, D)
 
 
 def cache_decode(q, kcache, vcache, wcache, pos, kprefix=None, vprefix=None, out=None, scale=None, workspace=None):
@@ -540,14 +558,13 @@ def cache_decode(q, kcache, vcache, wcache, pos, kprefix=None, vprefix=None, out
         raise ValueError("q must be [B,H,D] and the cache [B,Hkv,S,D]")
     if q.dtype != torch.bfloat16:
         raise TypeError("cache_decode takes bf16 q")
-    lib = _native.lib()
-    return _decode(lib.swa_cache_decode, lib.swa_cache_decode_workspace_bytes, True, q, kcache, vcache, wcache, pos,
+    return _decode(_native.lib().swa_cache_decode, True, q, kcache, vcache, wcache, pos,
                    kprefix, vprefix, S, Hkv, out, scale, workspace)
 
 
 def prefix_decode_workspace_bytes(B, H, Hkv, W, P, D):
     """Bytes of device workspace prefix_decode needs (0: none)."""
-    return int(_native.lib().swa_prefix_decode_workspace_bytes(B, H, Hkv, W, P, D))
+    return _decode_workspace(False, B, H, Hkv, W, P, D)
 
 
 def prefix_decode(q, kprefix, vprefix, kring, vring, pos, window, out=None, scale=None, workspace=None):
@@ -559,15 +576,15 @@ def prefix_decode(q, kprefix, vprefix, kring, vring, pos, window, out=None, scal
     prefix_decode_workspace_bytes(...) bytes, not shared by calls that may overlap. Returns
     out [B,H,D]."""
     torch = _torch()
-    if q.dim() != 3 or kring.dim() != 4:
+    qshape, shape = q.shape, kring.shape
+    if len(qshape) != 3 or len(shape) != 4:
         raise ValueError("q must be [B,H,D] and the rings [B,Hkv,W,D]")
-    Hkv = kring.shape[1]
-    if kring.shape != (q.shape[0], Hkv, window, q.shape[2]) or vring.shape != kring.shape:
+    Hkv = shape[1]
+    if shape[0] != qshape[0] or shape[2] != window or shape[3] != qshape[2] or vring.shape != shape:
         raise ValueError("rings must be [B,Hkv,W,D] with W = window")
     if q.dtype != torch.bfloat16 or kring.dtype != torch.bfloat16 or vring.dtype != torch.bfloat16:
         raise TypeError("prefix_decode takes bf16 q and rings")
-    lib = _native.lib()
-    return _decode(lib.swa_prefix_decode, lib.swa_prefix_decode_workspace_bytes, False, q, kring, vring, None, pos,
+    return _decode(_native.lib().swa_prefix_decode, False, q, kring, vring, None, pos,
                    kprefix, vprefix, int(window), Hkv, out, scale, workspace)
 
 
