@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kSeedThreads)
     __shared__ int sm_a[kWarps], sm_b[kWarps];
     __shared__ int sm_cta[2];     // this CTA's keys above and equal to the threshold
     __shared__ uint32_t sm_prefix;
-    __shared__ int sm_need;
+    __shared__ int sm_need, sm_found;  // of the keys that share the digits so far: to keep, in all
     const int rank = (int)(blockIdx.x % C);
     const int64_t bh = blockIdx.x / C, b = bh / Hkv, h = bh - b * Hkv;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -158,11 +158,11 @@ __global__ void __launch_bounds__(kSeedThreads)
         const int old = n - recent;  // positions 0 .. old-1 compete for S - recent slots; old > need
         const int run = ((old + C - 1) / C + 31) / 32 * 32;  // this CTA's: c0 .. c1-1
         const int c0 = min(old, rank * run), c1 = min(old, c0 + run);
-        int need = S - recent;
-        uint32_t prefix = 0;
-        for (int pass = 0; pass < 4; ++pass) {
+        int need = S - recent, found = 0;
+        uint32_t prefix = 0, mask = 0;
+        // until the digits so far single out exactly the keys still needed (mostly after three)
+        for (int pass = 0; pass < 4 && found != need; ++pass) {
             const int shift = 24 - 8 * pass;
-            const uint32_t mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
             int* mine = hist[pass & 1];
             if (tid < 256) mine[tid] = 0;
             __syncthreads();
@@ -195,21 +195,24 @@ __global__ void __launch_bounds__(kSeedThreads)
                     while (before + own[i] < need) before += own[i++];
                     sm_prefix = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
                     sm_need = need - before;
+                    sm_found = own[i];
                 }
             }
             __syncthreads();
             prefix = sm_prefix;
             need = sm_need;
+            found = sm_found;
+            mask = 0xFFFFFFFFu << shift;
             // The next pass clears the other histogram: every CTA has read that one, as it has
             // passed this pass's cluster barrier since.
         }
-        // Keep keys > prefix and the first `need` keys equal to it. Each warp takes one run of
+        // Keep keys > prefix in their digits so far and the first `need` equal to it. Each warp takes one run of
         // positions; the counts of the warps and CTAs before it say where its own go.
         const int wrun = ((c1 - c0 + kWarps - 1) / kWarps + 31) / 32 * 32;
         const int j0 = min(c1, c0 + warp * wrun), j1 = min(c1, j0 + wrun);
         int above = 0, equal = 0;
         for (int j = j0 + lane; j - lane < j1; j += 32) {
-            const uint32_t key = j < j1 ? weight_key(w[j]) : 0u;
+            const uint32_t key = j < j1 ? weight_key(w[j]) & mask : 0u;
             above += __popc(__ballot_sync(0xffffffffu, j < j1 && key > prefix));
             equal += __popc(__ballot_sync(0xffffffffu, j < j1 && key == prefix));
         }
@@ -236,7 +239,7 @@ __global__ void __launch_bounds__(kSeedThreads)
         const uint32_t below = (1u << lane) - 1u;
         for (int j = j0 + lane; j - lane < j1; j += 32) {
             const float x = j < j1 ? w[j] : 0.f;
-            const uint32_t key = weight_key(x);
+            const uint32_t key = weight_key(x) & mask;
             const uint32_t ba = __ballot_sync(0xffffffffu, j < j1 && key > prefix);
             const uint32_t be = __ballot_sync(0xffffffffu, j < j1 && key == prefix);
             const int a = na + __popc(ba & below), e = ne + __popc(be & below);
