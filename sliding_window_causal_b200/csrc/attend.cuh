@@ -300,11 +300,11 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_ke
     const int hk = (int)(unit - b * a.Hkv), nq = a.G;
     const int64_t row0 = b * a.H + hk * a.G;
     const int64_t pos = a.pos[b];
+    AttendState<D> st;
+    st.start(g < nq ? a.q + (row0 + g) * D : nullptr, t);  // beside the load of pos
     const int n = attend_slots(pos, a.S, a.status, tid == 0 && rank == 0);
     const int r0 = min(rank * a.chunk, n), r1 = min(r0 + a.chunk, n);
 
-    AttendState<D> st;
-    st.start(g < nq ? a.q + (row0 + g) * D : nullptr, t);
     if (sa.P0 > 0) {
         const int p0 = min(rank * sa.pchunk, sa.P0), p1 = min(p0 + sa.pchunk, sa.P0);
         st.keys(sa.pk + hk * sa.pk_head, sa.pv + hk * sa.pv_head, sa.pk_row, sa.pv_row, p0, p1, a.scale_log2, warp, g, t,
@@ -338,6 +338,15 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_ke
         }
         // the prefix's: of a lane, state `lane` of every 32 (the first 32 stay in registers)
         const float2 e0 = lane < a.NS ? __ldcg(ml + lane) : make_float2(-INFINITY, 0.f);
+        const bool writes = i % C == rank;  // the output row
+        constexpr int E = D / 32;           // its columns E lane ..
+        float v[8][E];                      // the prefix's first eight states, on their way meanwhile
+        auto fetch = [&](int s0) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+                if (s0 + y < a.NS) ldcg_vec(a.o + (row * a.NS + s0 + y) * D + E * lane, v[y]);
+        };
+        if (writes) fetch(0);
         float M = fmaxf(cm, e0.x);
         for (int s = 32 + lane; s < a.NS; s += 32) M = fmaxf(M, __ldcg(ml + s).x);
 #pragma unroll
@@ -351,16 +360,12 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_ke
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
         if (lane == 0) sm_lse[i] = M + log2f(L);
-        if (i % C != rank) continue;
-        constexpr int E = D / 32;  // columns E lane ..
+        if (!writes) continue;
         float acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        for (int s0 = 0; s0 < a.NS; s0 += 8) {  // the loads of eight states in flight
-            float v[8][E];
-#pragma unroll
-            for (int y = 0; y < 8; ++y)
-                if (s0 + y < a.NS) ldcg_vec(a.o + (row * a.NS + s0 + y) * D + E * lane, v[y]);
+        for (int s0 = 0; s0 < a.NS; s0 += 8) {
+            if (s0 > 0) fetch(s0);
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
                 if (s0 + y >= a.NS) break;
@@ -376,10 +381,10 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_ke
         }
         for (int r = 0; r < C; ++r) {
             const float f = __shfl_sync(0xffffffffu, cf, r);
-            float v[E];
-            ptx::cluster_ld_vec(ptx::cluster_addr(&join.o[0][i][E * lane], r), v);
+            float x[E];
+            ptx::cluster_ld_vec(ptx::cluster_addr(&join.o[0][i][E * lane], r), x);
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(v[e], f, acc[e]);
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(x[e], f, acc[e]);
         }
         uint32_t w[E / 2];
 #pragma unroll

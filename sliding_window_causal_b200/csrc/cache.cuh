@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6)
     const int64_t bh = blockIdx.x;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nt = blockDim.x;
     const int64_t P = pos[bh / Hkv];
+    const uint4 row = tid < vpr ? k[bh * vpr + tid] : tid < 2 * vpr ? v[bh * vpr + tid - vpr] : make_uint4(0, 0, 0, 0);
     float* w = wc + bh * S;
     int64_t* p = pc + bh * S;
     if (P >= S) {
@@ -102,8 +103,8 @@ __global__ void __launch_bounds__(kAppendThreads, 6)
     if (slot >= 0 && tid < 2 * vpr) {
         const int e = tid % vpr;
         const int64_t at = (bh * S + slot) * vpr + e;
-        if (tid < vpr) kc[at] = k[bh * vpr + e];
-        else vc[at] = v[bh * vpr + e];
+        if (tid < vpr) kc[at] = row;
+        else vc[at] = row;
     }
 }
 

@@ -179,6 +179,16 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     uint32_t loads = 0;  // producer: tiles issued
+    // The ring takes the tiles in the order in which the tensor core does, so that none waits for
+    // room behind one that is not needed yet: PAIR K0 V0 K1 V1 .., !PAIR K0 K1 V0 K2 V1 K3 ..
+    auto pos_k = [&](int t) -> uint32_t { return PAIR ? 2 * t : t == 0 ? 0 : 2 * t - 1; };
+    auto pos_v = [&](int t) -> uint32_t { return PAIR || t == n - 1 ? 2 * t + 1 : 2 * t + 2; };
+    // the tile at position L of 2 n: t for K_t, ~t for V_t
+    auto key_tile = [](int L, int n) -> int {
+        if (PAIR) return L & 1 ? ~(L >> 1) : L >> 1;
+        if (L == 2 * n - 1) return ~(n - 1);
+        return L < 2 ? L : L & 1 ? (L + 1) >> 1 : ~((L - 2) >> 1);
+    };
 
     if (warp < 4) {
         ptx::regs_dec<kPPRoleRegs>();
@@ -186,7 +196,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             if (lane == 0) {
                 // ------------------------------------------------------------ producer
                 bool ok = true;
-                for (int t = 0; t < 2 * n && ok; ++t) {
+                for (int L = 0; L < 2 * n && ok; ++L) {
+                    const int kt = key_tile(L, n);
+                    const bool is_v = kt < 0;
                     const uint32_t st = loads % NS;
                     if (loads >= (uint32_t)NS)
                         ok = ptx::mbar_wait(ring_empty + st, ((loads / NS) - 1) & 1, wait_limit_ns, abort_flag);
@@ -194,8 +206,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     uint8_t* dst = smem + Cf::kRingOff + st * Cf::kTileBytes;
                     ptx::mbar_arrive_expect_tx(ring_full + st, Cf::kTileBytes);
                     for (int c = 0; c < D / 64; ++c)
-                        ptx::tma_load_4d(dst + c * Cf::kBoxBytes, t & 1 ? &tm_v : &tm_k, ring_full + st, 64 * c,
-                                         128 * (t0 + (t >> 1)), hk, 0);
+                        ptx::tma_load_4d(dst + c * Cf::kBoxBytes, is_v ? &tm_v : &tm_k, ring_full + st, 64 * c,
+                                         128 * (t0 + (is_v ? ~kt : kt)), hk, 0);
                     ++loads;
                 }
                 if (!ok) {
@@ -254,7 +266,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     ptx::tc_commit_one(ring_empty + 0);
                 }
                 for (int j = 0; j < n && ok; ++j) {
-                    const uint32_t Lv = 2 * j + 1, Lk = 2 * j + 2;
+                    const uint32_t Lv = pos_v(j), Lk = pos_k(j + 1);
                     arrived(Lv);
                     if (j + 1 < n) arrived(Lk);
 #pragma unroll
@@ -270,14 +282,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 }
             } else {
                 for (int t = 0; t < 2 && t < n && ok; ++t) {
-                    arrived(2 * t);
+                    arrived(pos_k(t));
                     if (!ok) break;
-                    issue_s(t, 2 * t);
-                    ptx::tc_commit_one(ring_empty + (2 * t) % NS);
+                    issue_s(t, pos_k(t));
+                    ptx::tc_commit_one(ring_empty + pos_k(t) % NS);
                 }
                 for (int t = 0; t < n && ok; ++t) {
                     const int x = t & 1;
-                    const uint32_t Lv = 2 * t + 1, Lk = 2 * t + 4;
+                    const uint32_t Lv = pos_v(t), Lk = pos_k(t + 2);
                     arrived(Lv);
                     if (ok) issue_pv(x, Lv, t >> 1);
                     if (!ok) break;
