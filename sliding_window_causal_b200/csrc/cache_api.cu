@@ -150,7 +150,10 @@ int launch_key_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const f
     while (C < 8 && work * C < 2 * 148 && slices >= 8 * C) C *= 2;
     const int64_t units = B * Hkv * tiles;
     if (units * C > INT32_MAX) C = 1;
-    const int64_t grid = C > 1 ? units * C : units < 2 * 148 ? units : 2 * 148;
+    // Else CTAs that stay and go from tile to tile, which hides a tile's start, unless a tile is
+    // long (32 heads, W 4096, 66 slices: 628 us, 604 with a CTA to each tile; W 1024, 18: 194 and 220).
+    const bool stay = slices < 48 && units > 2 * 148;
+    const int64_t grid = C > 1 ? units * C : stay ? 2 * 148 : units;
     cudaLaunchConfig_t cfg = config(dim3((unsigned)grid), swa::kKwThreads, swa::KwCfg<D>::kSmemBytes, s);
     cudaLaunchAttribute at[1];
     cluster_of(&cfg, at, C);

@@ -151,18 +151,18 @@ __global__ void __launch_bounds__(kKwSimtThreads, 4)
 // lane is a key and its sum needs no exchange: no maximum, no second product, no atomics. The
 // queries that see the tile's keys come in slices of 64 rows (a head of the group, rows i0 ..),
 // two to a stage of 128 columns. Stage j uses ring slot, TMEM buffer and warpgroup j & 1. A CTA
-// goes on from one key tile to the next without a pause (C = 1). Roles:
+// may go on from one key tile to the next without a pause (C = 1). Roles:
 //   warp 0        TMA of the key tile and the query slices (lane 0); -lse log2(e) of each stage's
 //                 columns into shared memory
 //   warp 1        TMEM allocation and MMA issue
 //   warps 2 .. 9  two warpgroups: p = 2^(s c + nlse) and the row sums of every second stage
 // Bound: one exp a band pair on the special-function unit (16 a clock and SM), 2 x the time of
-// the product at D = 128. 32 heads of 16384 tokens, W 4096 (1.88 G exponentials): 582 us, 0.72
-// of that unit's rate; with 1, 2, 3 or 4 of each 8 exponentials as a polynomial on the FMA pipe
-// 588, 614, 665 and 681 us, as the warps' issue slots run out first. Two CTAs share an SM, so
-// that one's start and end overlap the other's work. Few keys and many queries: a cluster of C
-// CTAs splits the slices of one key tile and adds its sums in rank order through distributed
-// shared memory.
+// the product at D = 128. 32 heads of 16384 tokens, W 4096 (1.88 G exponentials): 0.60 to 0.64 ms
+// by the clock that the power cap leaves, two thirds of that unit's rate; with 1, 2, 3 or 4 of
+// each 8 exponentials as a polynomial on the FMA pipe an earlier form took 588, 614, 665 and 681
+// us against 582, as the warps' issue slots run out first. Two CTAs share an SM, so that one's
+// start and end overlap the other's work. Few keys and many queries: a cluster of C CTAs splits
+// the slices of one key tile and adds its sums in rank order through distributed shared memory.
 constexpr int kKwThreads = 320;
 constexpr int kKwSlice = 64;  // query rows of a slice
 constexpr int kKwStats = 8;   // stages of nlse in shared memory
@@ -289,20 +289,25 @@ __global__ void __launch_bounds__(kKwThreads, 2)
         // -------------------------------------------------------------------- loads, nlse
         for (int64_t r = 0, u; ok && (u = kw_unit(r, blockIdx.x / C, step)) < units; ++r) {
             const KwItem it(u, lens, BHk, H, Hkv, T, W, last, rank, C, status);
-            for (int j = 0; j < it.stages; ++j, ++J) {
-                const uint32_t y = J & 1;
-                float a[4];
+            // the lse of a stage are read two stages before they are stored
+            float a[2][4];
+            auto fetch = [&](int j, float (&r)[4]) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int s = it.s0 + 2 * j + x;
-                    a[2 * x] = a[2 * x + 1] = INFINITY;
+                    r[2 * x] = r[2 * x + 1] = INFINITY;
                     if (2 * j + x < it.slices) {
                         const int i = it.row(s) + lane;
                         const float* p = lse + ((int64_t)it.b * H + it.hk * (H / Hkv) + it.head(s)) * T + i;
-                        if (i <= it.i_hi) a[2 * x] = p[0];
-                        if (i + 32 <= it.i_hi) a[2 * x + 1] = p[32];
+                        if (i <= it.i_hi) r[2 * x] = p[0];
+                        if (i + 32 <= it.i_hi) r[2 * x + 1] = p[32];
                     }
                 }
+            };
+            fetch(0, a[0]);
+            fetch(1, a[1]);
+            for (int j = 0; j < it.stages && ok; ++j) {
+                const uint32_t y = J & 1;
                 // Stage J - 2 has its scores: ring slot y is free, and so is the nlse slot of stage
                 // J - 8: those scores were computed after the warpgroup had read stage J - 4's,
                 // which it does after it has finished stage J - 6. Before the first stage of a
@@ -330,9 +335,13 @@ __global__ void __launch_bounds__(kKwThreads, 2)
                 if (j == 0) ++n_k;
                 float* nl = sm_nl + 128 * (J % kKwStats) + lane;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) nl[32 * x] = a[x] * -1.4426950408889634f;
+                for (int x = 0; x < 4; ++x) nl[32 * x] = a[0][x] * -1.4426950408889634f;
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(s_full + y);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) a[0][x] = a[1][x];
+                fetch(j + 2, a[1]);
+                ++J;
             }
         }
         if (!ok && lane == 0) {
@@ -378,31 +387,42 @@ __global__ void __launch_bounds__(kKwThreads, 2)
         const int quarter = warp & 3, y = (warp - 2) >> 2, row = 32 * quarter + lane;
         const uint32_t col = tmem + ((uint32_t)(32 * quarter) << 16) + 128 * y;
         for (int64_t r = 0, u; ok && (u = kw_unit(r, blockIdx.x / C, step)) < units; ++r) {
-            const KwItem it(u, lens, BHk, H, Hkv, T, W, last, rank, C, status);
-            const int jk = it.j0 + row;
-            float* to = out + (it.b * Hkv + it.hk) * T + jk;
-            if (it.stages == 0) {
+            int jk, i_lo, per_head, slices, stages, at, full_lo, full_hi, see, n;
+            const int first = (y - J) & 1;  // this warpgroup's first stage of the unit
+            {
+                const KwItem it(u, lens, BHk, H, Hkv, T, W, last, rank, C, status);
+                jk = it.j0 + row;
+                n = it.n;
+                i_lo = it.i_lo;
+                per_head = it.per_head;
+                slices = it.slices;
+                stages = it.stages;
+                // a slice is full when every key of the tile is in the band of each of its rows
+                full_lo = it.j0 + 127;
+                full_hi = min(it.j0 + W - 1, it.i_hi) - (kKwSlice - 1);
+                see = min(jk + W - 1, it.i_hi);  // this key is seen by queries jk .. see
+                at = stages ? (it.s0 + 2 * first) % per_head : 0;  // slice of its head, at the stage's first
+            }
+            auto put = [&](float w) {  // a key past the stream's end may have met anything in its row
+                if (jk < T) out[u % BHk * T + jk] = jk < n ? w : 0.f;
+            };
+            if (stages == 0) {
                 if (C == 1) {
-                    if (y == 0 && jk < T) *to = 0.f;
+                    if (y == 0) put(0.f);
                 } else {
                     sm_red[128 * y + row] = 0.f;
                 }
                 continue;
             }
-            // a slice is full when every key of the tile is in the band of each of its rows
-            const int full_lo = it.j0 + 127, full_hi = min(it.j0 + W - 1, it.i_hi) - (kKwSlice - 1);
-            const int see = min(jk + W - 1, it.i_hi);  // this key is seen by queries jk .. see
-            const int first = (y - J) & 1;             // this warpgroup's first stage of the unit
-            int at = (it.s0 + 2 * first) % it.per_head;  // slice of its head, at the stage's first
             ptx::f32x2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
-            for (int j = first; j < it.stages; j += 2) {
+            for (int j = first; j < stages; j += 2) {
                 const uint32_t Jj = J + j;
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full + y, (Jj >> 1) & 1, wait_limit_ns, abort_flag));
                 if (!ok) break;
                 ptx::tc_fence_after();
-                const int at1 = at + 1 < it.per_head ? at + 1 : 0;
-                const int i0 = it.i_lo + kKwSlice * at, i1 = it.i_lo + kKwSlice * at1;
-                const bool two = it.slices - 2 * j >= 2;
+                const int at1 = at + 1 < per_head ? at + 1 : 0;
+                const int i0 = i_lo + kKwSlice * at, i1 = i_lo + kKwSlice * at1;
+                const bool two = slices - 2 * j >= 2;
                 const bool full0 = i0 >= full_lo && i0 <= full_hi, full1 = i1 >= full_lo && i1 <= full_hi;
                 const float* nl = sm_nl + 128 * (Jj % kKwStats);
                 if (full0 && full1 && two) {
@@ -438,7 +458,7 @@ __global__ void __launch_bounds__(kKwThreads, 2)
                     if (lane == 0) ptx::mbar_arrive(s_read + y);
                 }
                 at += 4;
-                while (at >= it.per_head) at -= it.per_head;
+                while (at >= per_head) at -= per_head;
             }
             if (!ok) break;
             const float mine = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
@@ -453,17 +473,16 @@ __global__ void __launch_bounds__(kKwThreads, 2)
                 const uint32_t set = n_k % kKwSets;
                 float* red = sm_red + 128 * set + row;
                 uint64_t* full = red_full + 4 * set + quarter;
-                if (((J + it.stages - 1) & 1) != (uint32_t)y) {
+                if (((J + stages - 1) & 1) != (uint32_t)y) {
                     *red = mine;
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(full);
                 } else {
                     ok = __all_sync(0xffffffffu, ptx::mbar_wait(full, (n_k / kKwSets) & 1, wait_limit_ns, abort_flag));
-                    // a key past the stream's end may have met anything in its row
-                    if (ok && jk < T) *to = jk < it.n ? *red + mine : 0.f;
+                    if (ok) put(*red + mine);
                 }
             }
-            J += it.stages;
+            J += stages;
             ++n_k;
         }
         if (!ok) {
