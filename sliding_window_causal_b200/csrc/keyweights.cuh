@@ -7,7 +7,9 @@
 // key_weights_tc_kernel (bf16): tcgen05 score tiles, below.
 // key_weights_simt_kernel (fp32): FMA on 64-key x 64-query score tiles. A CTA, or a cluster that
 // splits the query tiles, owns 64 keys, so every sum has one owner and a fixed order. Small
-// calls are bound by the latency of a tile's loads.
+// calls are bound by the latency of a tile's loads (2 streams, 4 heads, 777 tokens, D 80, W 200:
+// 28 us; 2 heads of 2000 tokens, W 2000: 54 us with clusters of 8, 213 without), large ones by
+// instruction issue (16 heads of 2000 tokens, D 64, W 1000, 3 GFLOP of multiply-adds: 174 us).
 #pragma once
 #include <cuda_bf16.h>
 #include <math.h>

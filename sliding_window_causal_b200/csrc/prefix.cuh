@@ -17,6 +17,10 @@
 // softmax of lanes 0 and 1 (prefix_tile, a row a thread). Q goes to shared memory by plain loads, in the layout of a
 // TMA tile, since G query heads of 128 / G streams are no box for every G.
 //
+// Measured, D = 128: 128 streams of 32 heads, 4 to a key head, behind 65536 keys (PAIR, 137 GFLOP):
+// 0.118 ms, 1.16 PFLOP/s; hi + lo parts there 0.148 ms, P handed over in 1 or 4 parts instead of 2
+// 0.125 and 0.122 ms. 64 streams of 32 heads (!PAIR): 72 us more for 24576 more keys, 5.6 TB/s.
+//
 // P is rounded to bf16. !PAIR carries it as hi + lo parts (2^-16), for the second product costs
 // nothing there. PAIR is bound by tensor core and exponentials and carries one part: each weight
 // is off by up to 2^-8 of itself, which in the output is at most as much as the rounding of the
