@@ -173,8 +173,7 @@ struct AttendState {
 };
 
 // The states of a CTA's warps, joined: done(query, d, M, L, A) for every 4 columns d of the
-// first nq queries, once each. done runs after every read of sm_m and sm_l, and after the reads
-// of its own columns of o.
+// first nq queries, once each, and may overwrite these columns of o[0].
 template <int D>
 struct AttendJoin {
     float m[kAttendWarps][kAttendQueries], l[kAttendWarps][kAttendQueries];
@@ -269,7 +268,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) attend_ke
 // but the prefix's, one launch, no traffic beyond the inputs and outputs. G <= 8. 64 streams, 32
 // heads, 4096 slots, D = 128, with weights: 643 us, 6.8 TB/s (attend_kernel and finish_kernel,
 // which write and read the scores once more: 701 us). Few slots a CTA leave the latency of its
-// chain of loads: 32 key heads of 32 streams, 256 slots: 27 us for 134 MB.
+// chain of loads: 1024 (stream, key head)s of 256 slots take 27 us for 134 MB.
 struct StreamArgs {
     AttendArgs a;                 // slots; ml, o, NS: the np partial states of a row
     const __nv_bfloat16* pk;      // the prefix: (h, t) strides
@@ -358,7 +357,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_ke
         float L = fmaf(cl, cf, e0.y * f0);
         for (int s = 32 + lane; s < a.NS; s += 32) {
             const float2 e = __ldcg(ml + s);
-            if (e.x != -INFINITY) L = fmaf(e.y, ptx::ex2(e.x - M), L);
+            L = fmaf(e.y, e.x == -INFINITY ? 0.f : ptx::ex2(e.x - M), L);
         }
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
@@ -420,9 +419,9 @@ __device__ __forceinline__ float2 finish_ml(const float2* ml, int NS, int lane) 
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
     float L = 0.f;
-    for (int s = lane; s < NS; s += 32) {
+    for (int s = lane; s < NS; s += 32) {  // l is 0 without a key, NaN where all its scores are
         const float2 e = __ldcg(ml + s);
-        if (e.x != -INFINITY) L = fmaf(e.y, ptx::ex2(e.x - M), L);
+        L = fmaf(e.y, e.x == -INFINITY ? 0.f : ptx::ex2(e.x - M), L);
     }
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);

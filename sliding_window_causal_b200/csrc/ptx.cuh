@@ -280,8 +280,8 @@ __device__ __forceinline__ void cluster_ld_vec(uint32_t at, float (&v)[4]) {
 __device__ __forceinline__ void cluster_ld_vec(uint32_t at, float (&v)[2]) {
     asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(at));
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------- math
 __device__ __forceinline__ float ex2(float x) {

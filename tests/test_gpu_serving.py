@@ -390,6 +390,32 @@ def test_decode_reports_a_negative_position():
         assert torch.equal(w[1], wc[1])
 
 
+@pytest.mark.parametrize("B,G,P", [(2, 1, 0), (2, 9, 0), (2, 2, 100), (40, 2, 4000), (80, 2, 2000), (3, 12, 5000)])
+def test_decode_of_nan_keys(B, G, P):
+    """A NaN key that a query sees makes its output NaN, wherever the key is and also where every
+    key of a split is NaN; the other streams' and heads' outputs do not change."""
+    Hkv, D, S = 2, 64, 700
+    g = gen(39)
+    q, kc, vc = rand(g, B, Hkv * G, D), rand(g, B, Hkv, S, D), rand(g, B, Hkv, S, D)
+    kp, vp = (rand(g, Hkv, P, D), rand(g, Hkv, P, D)) if P else (None, None)
+    pos = torch.full((B,), 2 * S, device=DEV)
+    good = swa.prefix_decode(q, kp, vp, kc, vc, pos, S)
+    for n in (1, 640):
+        bad = kc.clone()
+        bad[0, 1, :n] = math.nan
+        wc = torch.zeros(B, Hkv, S, device=DEV)
+        for out in (swa.prefix_decode(q, kp, vp, bad, vc, pos, S), swa.cache_decode(q, bad, vc, wc, pos, kp, vp)):
+            assert bool(out[0, G:].isnan().all())
+            assert torch.equal(out[0, :G], good[0, :G]) and torch.equal(out[1:], good[1:])
+        assert bool(wc[0, 1].isnan().all()) and not bool(wc[0, 0].isnan().any()) and not bool(wc[1:].isnan().any())
+    if P:
+        bad = kp.clone()
+        bad[1, P // 2] = math.nan
+        out = swa.prefix_decode(q, bad, vp, kc, vc, pos, S)
+        assert bool(out[:, G:].isnan().all()) and torch.equal(out[:, :G], good[:, :G])
+    swa.device_status()
+
+
 def test_decode_of_the_last_position():
     B, H, D, S = 2, 2, 64, 33
     g = gen(37)
