@@ -140,18 +140,20 @@ int launch_key_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const f
     auto* kernel = swa::key_weights_tc_kernel<D>;
     if (int rc = allow_smem(reinterpret_cast<const void*>(kernel), swa::KwCfg<D>::kSmemBytes)) return rc;
     const int64_t tiles = (T + 127) / 128;
-    // A cluster splits a key tile's query slices while the working CTAs (the tiles that some
-    // counted query sees, at most) do not fill the 148 SMs twice and each keeps 4 slices or more.
+    // A cluster splits a key tile's query slices: while the working CTAs (the tiles that some
+    // counted query sees, at most) do not give each SM one, if each keeps 4 slices or more (4 heads
+    // of 1000 tokens, W 300: 7.6 us, 8.4 whole); while they do not give each SM two, if each keeps
+    // 32 (4 key heads of 6000 tokens: 58 us, 90 whole; 24 slices a tile, 272 tiles: 29 us, 26 whole).
     const int64_t seen = (int64_t)W + last < T ? (int64_t)W + last : T;
     const int64_t work = B * Hkv * ((seen + 127) / 128);
     const int64_t rows = 127 + (int64_t)(W < last ? W : last);
     const int64_t slices = H / Hkv * ((rows + swa::kKwSlice - 1) / swa::kKwSlice);
     int C = 1;
-    while (C < 8 && work * C < 2 * 148 && slices >= 8 * C) C *= 2;
+    while (C < 8 && work * C < 2 * 148 && slices >= (work * C <= 74 ? 4 : 32) * C) C *= 2;
     const int64_t units = B * Hkv * tiles;
     if (units * C > INT32_MAX) C = 1;
     // Else CTAs that stay and go from tile to tile, which hides a tile's start, unless a tile is
-    // long (32 heads, W 4096, 66 slices: 628 us, 604 with a CTA to each tile; W 1024, 18: 194 and 220).
+    // long (32 heads, W 4096, 66 slices: 599 us, 580 with a CTA to each tile; W 1024, 18: 183 and 211).
     const bool stay = slices < 48 && units > 2 * 148;
     const int64_t grid = C > 1 ? units * C : stay ? 2 * 148 : units;
     cudaLaunchConfig_t cfg = config(dim3((unsigned)grid), swa::kKwThreads, swa::KwCfg<D>::kSmemBytes, s);

@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(kKwSimtThreads, 4)
 //   warp 1        TMEM allocation and MMA issue
 //   warps 2 .. 9  two warpgroups: p = 2^(s c + nlse) and the row sums of every second stage
 // Bound: one exp a band pair on the special-function unit (16 a clock and SM), 2 x the time of
-// the product at D = 128. 32 heads of 16384 tokens, W 4096 (1.88 G exponentials): 0.60 to 0.64 ms
-// by the clock that the power cap leaves, two thirds of that unit's rate; with 1, 2, 3 or 4 of
+// the product at D = 128. 32 heads of 16384 tokens, W 4096 (1.88 G exponentials): 0.58 to 0.62 ms
+// by the clock that the power cap leaves, 0.7 of that unit's rate; with 1, 2, 3 or 4 of
 // each 8 exponentials as a polynomial on the FMA pipe an earlier form took 588, 614, 665 and 681
 // us against 582, as the warps' issue slots run out first. Two CTAs share an SM, so that one's
 // start and end overlap the other's work. Few keys and many queries: a cluster of C CTAs splits
@@ -210,8 +210,6 @@ struct KwItem {
         slices = (int)(all * (rank + 1) / C) - s0;
         stages = (slices + 1) / 2;
     }
-    __device__ __forceinline__ int head(int s) const { return s / per_head; }
-    __device__ __forceinline__ int row(int s) const { return i_lo + kKwSlice * (s % per_head); }
 };
 
 // The r-th unit of CTA (or cluster) g of G, in a snake order that evens out slowly changing work.
@@ -291,59 +289,73 @@ __global__ void __launch_bounds__(kKwThreads, 2)
         // -------------------------------------------------------------------- loads, nlse
         for (int64_t r = 0, u; ok && (u = kw_unit(r, blockIdx.x / C, step)) < units; ++r) {
             const KwItem it(u, lens, BHk, H, Hkv, T, W, last, rank, C, status);
-            // the lse of a stage are read two stages before they are stored
+            if (it.stages == 0) continue;
+            // The slices in order: of the loads (at, head) and, two stages ahead, of the lse (lat,
+            // row), which are read long before they are stored.
+            int at = it.s0 % it.per_head, head = (int)it.hk * (H / Hkv) + it.s0 / it.per_head;
+            int lat = at, left = it.slices;
+            const float* row = lse + ((int64_t)it.b * H + head) * T + lane;
             float a[2][4];
-            auto fetch = [&](int j, float (&r)[4]) {
+            auto fetch = [&](float (&v)[4]) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int s = it.s0 + 2 * j + x;
-                    r[2 * x] = r[2 * x + 1] = INFINITY;
-                    if (2 * j + x < it.slices) {
-                        const int i = it.row(s) + lane;
-                        const float* p = lse + ((int64_t)it.b * H + it.hk * (H / Hkv) + it.head(s)) * T + i;
-                        if (i <= it.i_hi) r[2 * x] = p[0];
-                        if (i + 32 <= it.i_hi) r[2 * x + 1] = p[32];
+                    v[2 * x] = v[2 * x + 1] = INFINITY;
+                    if (left > 0) {
+                        const int i = it.i_lo + kKwSlice * lat;
+                        if (i + lane <= it.i_hi) v[2 * x] = row[i];
+                        if (i + 32 + lane <= it.i_hi) v[2 * x + 1] = row[i + 32];
+                        --left;
+                        if (++lat == it.per_head) {
+                            lat = 0;
+                            row += T;
+                        }
                     }
                 }
             };
-            fetch(0, a[0]);
-            fetch(1, a[1]);
-            for (int j = 0; j < it.stages && ok; ++j) {
-                const uint32_t y = J & 1;
-                // Stage J - 2 has its scores: ring slot y is free, and so is the nlse slot of stage
-                // J - 8: those scores were computed after the warpgroup had read stage J - 4's,
-                // which it does after it has finished stage J - 6. Before the first stage of a
-                // unit stage J - 1 has too, so that the key tile may be replaced.
-                const uint32_t P = j == 0 ? J - 1 : J - 2;
-                if (J >= (j == 0 ? 1u : 2u))
-                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full + (P & 1), (P >> 1) & 1, wait_limit_ns, abort_flag));
-                if (!ok) break;
-                if (lane == 0) {
-                    if (j == 0) {
-                        ptx::mbar_arrive_expect_tx(k_full, Cf::kTileBytes);
-                        for (int c = 0; c < D / 64; ++c)
-                            ptx::tma_load_4d(smem + c * Cf::kBoxBytes, &tm_k, k_full, 64 * c, it.j0, (int)it.hk, (int)it.b);
+            fetch(a[0]);
+            fetch(a[1]);
+            for (int jj = 0; jj < it.stages && ok; jj += 2) {
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const int j = jj + z;
+                    if (j >= it.stages || !ok) break;
+                    const uint32_t y = J & 1;
+                    // Stage J - 2 has its scores: ring slot y is free, and so is the nlse slot of stage
+                    // J - 8: those scores were computed after the warpgroup had read stage J - 4's,
+                    // which it does after it has finished stage J - 6. Before the first stage of a
+                    // unit stage J - 1 has too, so that the key tile may be replaced.
+                    const uint32_t P = j == 0 ? J - 1 : J - 2;
+                    if (J >= (j == 0 ? 1u : 2u))
+                        ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full + (P & 1), (P >> 1) & 1, wait_limit_ns, abort_flag));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (j == 0) {
+                            ptx::mbar_arrive_expect_tx(k_full, Cf::kTileBytes);
+                            for (int c = 0; c < D / 64; ++c)
+                                ptx::tma_load_4d(smem + c * Cf::kBoxBytes, &tm_k, k_full, 64 * c, it.j0, (int)it.hk, (int)it.b);
+                        }
+                        uint8_t* dst = smem + Cf::kRingOff + y * Cf::kTileBytes;
+                        const int here = min(2, it.slices - 2 * j);
+                        ptx::mbar_arrive_expect_tx(ring_full + y, here * Cf::kSliceBytes);
+                        for (int x = 0; x < here; ++x) {
+                            for (int c = 0; c < D / 64; ++c)
+                                ptx::tma_load_4d(dst + c * Cf::kBoxBytes + x * (Cf::kBoxBytes / 2), &tm_q, ring_full + y,
+                                                 64 * c, it.i_lo + kKwSlice * at, head, (int)it.b);
+                            if (++at == it.per_head) {
+                                at = 0;
+                                ++head;
+                            }
+                        }
                     }
-                    uint8_t* dst = smem + Cf::kRingOff + y * Cf::kTileBytes;
-                    const int here = min(2, it.slices - 2 * j);
-                    ptx::mbar_arrive_expect_tx(ring_full + y, here * Cf::kSliceBytes);
-                    for (int x = 0; x < here; ++x) {
-                        const int s = it.s0 + 2 * j + x;
-                        for (int c = 0; c < D / 64; ++c)
-                            ptx::tma_load_4d(dst + c * Cf::kBoxBytes + x * (Cf::kBoxBytes / 2), &tm_q, ring_full + y,
-                                             64 * c, it.row(s), (int)it.hk * (H / Hkv) + it.head(s), (int)it.b);
-                    }
+                    if (j == 0) ++n_k;
+                    float* nl = sm_nl + 128 * (J % kKwStats) + lane;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) nl[32 * x] = a[z][x] * -1.4426950408889634f;
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(s_full + y);
+                    fetch(a[z]);
+                    ++J;
                 }
-                if (j == 0) ++n_k;
-                float* nl = sm_nl + 128 * (J % kKwStats) + lane;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) nl[32 * x] = a[0][x] * -1.4426950408889634f;
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(s_full + y);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) a[0][x] = a[1][x];
-                fetch(j + 2, a[1]);
-                ++J;
             }
         }
         if (!ok && lane == 0) {
