@@ -360,16 +360,17 @@ def _same_device(dense, strided=()):
     return d
 
 
-def _launch(index, fn, *args):
-    """fn(*args, current stream) with device `index` as the current one."""
+@functools.lru_cache(maxsize=None)
+def _cuda():
+    """torch's calls for the current device's index and a device's current stream, as integers."""
     torch = _torch()
-    if index == torch._C._cuda_getDevice():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if rc:
-        check(rc)
+    return torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _elsewhere(index, fn, *args):
+    """fn(*args, current stream) with device `index` as the current one, which it is not."""
+    with _torch().cuda.device(index):
+        return fn(*args, _cuda()[1](index))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -412,12 +413,16 @@ def key_weights(q, k, lse, window, lens=None, last=None, scale=None):
     if lens is not None:
         _positions(lens, B, "lens")
     dev = _same_device((lse,) if lens is None else (lse, lens), (q, k))
-    out = lse.new_empty((B, Hkv, T))
+    out = torch.empty(B, Hkv, T, dtype=torch.float32, device=lse.device)
     sc = 1.0 / D ** 0.5 if scale is None else float(scale)
     strides = None if q.is_contiguous() and k.is_contiguous() else _bht_strides(q, k)
-    _launch(dev, _native.lib().swa_key_weights, q.data_ptr(), k.data_ptr(), lse.data_ptr(),
-            None if lens is None else lens.data_ptr(), out.data_ptr(), B, H, Hkv, T, D, int(window),
-            max(T, 1) if last is None else int(last), sc, strides, _dtype_code(q))
+    fn = _native.lib().swa_key_weights
+    args = (q.data_ptr(), k.data_ptr(), lse.data_ptr(), None if lens is None else lens.data_ptr(), out.data_ptr(),
+            B, H, Hkv, T, D, int(window), max(T, 1) if last is None else int(last), sc, strides, _dtype_code(q))
+    current, stream = _cuda()
+    rc = fn(*args, stream(dev)) if current() == dev else _elsewhere(dev, fn, *args)
+    if rc:
+        check(rc)
     return out
 
 
@@ -460,9 +465,14 @@ def cache_seed(k, v, weights, kcache, vcache, wcache, pcache, recent, lens=None)
         dense += (lens,)
     dev = _same_device(dense, (k, v))
     strides = None if k.is_contiguous() and v.is_contiguous() else _bht_strides(k, v)
-    _launch(dev, _native.lib().swa_cache_seed, k.data_ptr(), v.data_ptr(), weights.data_ptr(),
-            None if lens is None else lens.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), wcache.data_ptr(),
-            pcache.data_ptr(), B, Hkv, T, D, S, int(recent), strides)
+    fn = _native.lib().swa_cache_seed
+    args = (k.data_ptr(), v.data_ptr(), weights.data_ptr(), None if lens is None else lens.data_ptr(),
+            kcache.data_ptr(), vcache.data_ptr(), wcache.data_ptr(), pcache.data_ptr(), B, Hkv, T, D, S, int(recent),
+            strides)
+    current, stream = _cuda()
+    rc = fn(*args, stream(dev)) if current() == dev else _elsewhere(dev, fn, *args)
+    if rc:
+        check(rc)
 
 
 def cache_append(k, v, kcache, vcache, wcache, pcache, pos, recent):
@@ -480,18 +490,26 @@ def cache_append(k, v, kcache, vcache, wcache, pcache, pos, recent):
         raise TypeError("the cache's keys and values are bf16")
     _positions(pos, B)
     dev = _same_device((k, v, kcache, vcache, wcache, pcache, pos))
-    slots = pos.new_empty((B, Hkv))
-    _launch(dev, _native.lib().swa_cache_append, k.data_ptr(), v.data_ptr(), kcache.data_ptr(), vcache.data_ptr(),
-            wcache.data_ptr(), pcache.data_ptr(), pos.data_ptr(), slots.data_ptr(), B, Hkv, D, S, int(recent))
+    slots = torch.empty(B, Hkv, dtype=torch.int64, device=pos.device)
+    fn = _native.lib().swa_cache_append
+    args = (k.data_ptr(), v.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), wcache.data_ptr(), pcache.data_ptr(),
+            pos.data_ptr(), slots.data_ptr(), B, Hkv, D, S, int(recent))
+    current, stream = _cuda()
+    rc = fn(*args, stream(dev)) if current() == dev else _elsewhere(dev, fn, *args)
+    if rc:
+        check(rc)
     return slots
 
 
 def _decode(fn, weighted, q, kc, vc, wc, pos, kprefix, vprefix, S, Hkv, out, scale, workspace):
     """The two decodes' common part: prefix, buffers and call."""
     torch = _torch()
+    bf16 = torch.bfloat16
     B, H, D = shape = q.shape
-    _heads(H, Hkv)
-    _positions(pos, B)
+    if Hkv < 1 or H % Hkv:
+        _heads(H, Hkv)
+    if pos.dtype != torch.int64 or pos.shape != (B,):
+        _positions(pos, B)
     dense = [q, kc, vc, pos]
     if weighted:
         dense.append(wc)
@@ -500,7 +518,7 @@ def _decode(fn, weighted, q, kc, vc, wc, pos, kprefix, vprefix, S, Hkv, out, sca
         pshape = kprefix.shape
         if len(pshape) != 3 or vprefix.shape != pshape or pshape[0] != Hkv or pshape[2] != D:
             raise ValueError("kprefix and vprefix must share one [Hkv,P,D] shape")
-        if kprefix.dtype != torch.bfloat16 or vprefix.dtype != torch.bfloat16:
+        if kprefix.dtype != bf16 or vprefix.dtype != bf16:
             raise TypeError("the prefix is bf16")
         P = pshape[1]
         if P:
@@ -531,11 +549,15 @@ def _decode(fn, weighted, q, kc, vc, wc, pos, kprefix, vprefix, S, Hkv, out, sca
             ws = workspace.data_ptr()
     sc = 1.0 / D ** 0.5 if scale is None else float(scale)
     if weighted:
-        _launch(dev, fn, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), wc.data_ptr(), pos.data_ptr(), kp, vp,
-                out.data_ptr(), ws, have, B, H, Hkv, S, P, D, sc, strides)
+        args = (q.data_ptr(), kc.data_ptr(), vc.data_ptr(), wc.data_ptr(), pos.data_ptr(), kp, vp, out.data_ptr(), ws,
+                have, B, H, Hkv, S, P, D, sc, strides)
     else:
-        _launch(dev, fn, q.data_ptr(), kp, vp, kc.data_ptr(), vc.data_ptr(), pos.data_ptr(), out.data_ptr(), ws, have,
-                B, H, Hkv, S, P, D, sc, strides)
+        args = (q.data_ptr(), kp, vp, kc.data_ptr(), vc.data_ptr(), pos.data_ptr(), out.data_ptr(), ws, have, B, H, Hkv,
+                S, P, D, sc, strides)
+    current, stream = _cuda()
+    rc = fn(*args, stream(dev)) if current() == dev else _elsewhere(dev, fn, *args)
+    if rc:
+        check(rc)
     return out
 
 
@@ -582,7 +604,8 @@ def prefix_decode(q, kprefix, vprefix, kring, vring, pos, window, out=None, scal
     Hkv = shape[1]
     if shape[0] != qshape[0] or shape[2] != window or shape[3] != qshape[2] or vring.shape != shape:
         raise ValueError("rings must be [B,Hkv,W,D] with W = window")
-    if q.dtype != torch.bfloat16 or kring.dtype != torch.bfloat16 or vring.dtype != torch.bfloat16:
+    bf16 = torch.bfloat16
+    if q.dtype != bf16 or kring.dtype != bf16 or vring.dtype != bf16:
         raise TypeError("prefix_decode takes bf16 q and rings")
     return _decode(_native.lib().swa_prefix_decode, False, q, kring, vring, None, pos,
                    kprefix, vprefix, int(window), Hkv, out, scale, workspace)
