@@ -381,12 +381,21 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_ke
                 for (int e = 0; e < E; ++e) acc[e] = fmaf(v[y][e], f, acc[e]);
             }
         }
-        for (int r = 0; r < C; ++r) {
-            const float f = __shfl_sync(0xffffffffu, cf, r);
-            float x[E];
-            ptx::cluster_ld_vec(ptx::cluster_addr(&join.o[0][i][E * lane], r), x);
+        // the cluster's states, all loads in flight together
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(x[e], f, acc[e]);
+        for (int r = 0; r < 8; ++r) {
+            if (r < C) {
+                ptx::cluster_ld_vec(ptx::cluster_addr(&join.o[0][i][E * lane], r), v[r]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[r][e] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const float f = __shfl_sync(0xffffffffu, cf, r);  // 0 past the cluster
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(v[r][e], f, acc[e]);
         }
         uint32_t w[E / 2];
 #pragma unroll

@@ -176,10 +176,14 @@ __global__ void __launch_bounds__(kSeedThreads)
             }
             sync();
             if (tid < 256) {
-                int sum = 0;
-                if (C > 1)
-                    for (int r = 0; r < C; ++r) sum += __float_as_int(ptx::cluster_ld(ptx::cluster_addr(&mine[tid], r)));
-                else sum = mine[tid];
+                int sum = mine[tid];
+                if (C > 1) {  // the loads of all CTAs' counts in flight together
+                    int x[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        x[r] = r < C ? __float_as_int(ptx::cluster_ld(ptx::cluster_addr(&mine[tid], r))) : 0;
+                    sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+                }
                 all[tid] = sum;
             }
             __syncthreads();
@@ -225,21 +229,26 @@ __global__ void __launch_bounds__(kSeedThreads)
             sm_b[warp] = equal;
         }
         __syncthreads();
-        if (tid < 2) {
-            int sum = 0;
-            for (int x = 0; x < kWarps; ++x) sum += tid ? sm_b[x] : sm_a[x];
-            sm_cta[tid] = sum;
+        if (warp == 0) {
+            const int a = __reduce_add_sync(0xffffffffu, lane < kWarps ? sm_a[lane] : 0);
+            const int b = __reduce_add_sync(0xffffffffu, lane < kWarps ? sm_b[lane] : 0);
+            if (lane == 0) {
+                sm_cta[0] = a;
+                sm_cta[1] = b;
+            }
         }
         sync();
         int na = 0, ne = 0;  // kept above and seen equal before this position
-        for (int r = 0; r < rank; ++r) {
-            na += __float_as_int(ptx::cluster_ld(ptx::cluster_addr(&sm_cta[0], r)));
-            ne += __float_as_int(ptx::cluster_ld(ptx::cluster_addr(&sm_cta[1], r)));
+        if (lane < rank) {  // lane: CTA `lane` of the cluster
+            na = __float_as_int(ptx::cluster_ld(ptx::cluster_addr(&sm_cta[0], lane)));
+            ne = __float_as_int(ptx::cluster_ld(ptx::cluster_addr(&sm_cta[1], lane)));
         }
-        for (int x = 0; x < warp; ++x) {
-            na += sm_a[x];
-            ne += sm_b[x];
+        if (lane < warp) {  // and warp `lane` of this CTA
+            na += sm_a[lane];
+            ne += sm_b[lane];
         }
+        na = __reduce_add_sync(0xffffffffu, na);
+        ne = __reduce_add_sync(0xffffffffu, ne);
         const uint32_t below = (1u << lane) - 1u;
         for (int j = j0 + lane; j - lane < j1; j += 32) {
             const float x = j < j1 ? w[j] : 0.f;

@@ -138,8 +138,12 @@ __global__ void __launch_bounds__(kKwSimtThreads, 4)
         __syncthreads();
     }
     if (rank == 0 && tid < kKwTile && j0 + tid < T) {
-        float w = sm_sum[tid];
-        for (int r = 1; r < C; ++r) w += ptx::cluster_ld(ptx::cluster_addr(sm_sum + tid, r));
+        float x[8];  // all loads in flight together
+#pragma unroll
+        for (int r = 0; r < 8; ++r) x[r] = r < C ? ptx::cluster_ld(ptx::cluster_addr(sm_sum + tid, r)) : 0.f;
+        float w = C > 1 ? x[0] : sm_sum[tid];
+#pragma unroll
+        for (int r = 1; r < 8; ++r) w += x[r];
         out[bh * T + j0 + tid] = w;
     }
     if (C > 1) {  // the other CTAs' sums are read before they leave
@@ -531,11 +535,16 @@ __global__ void __launch_bounds__(kKwThreads, 2)
         ptx::cluster_wait();
         if (rank == 0 && tid < 128) {
             const KwItem it(blockIdx.x / C, lens, BHk, H, Hkv, T, W, last, rank, C, status);
-            float w = sm_red[tid] + sm_red[128 + tid];
-            for (int r = 1; r < C; ++r) {
-                const uint32_t from = ptx::cluster_addr(sm_red + tid, r);
-                w += ptx::cluster_ld(from) + ptx::cluster_ld(from + 512);
+            float x[8][2];  // all loads in flight together
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const uint32_t from = ptx::cluster_addr(sm_red + tid, r < C ? r : 0);
+                x[r][0] = r < C ? ptx::cluster_ld(from) : 0.f;
+                x[r][1] = r < C ? ptx::cluster_ld(from + 512) : 0.f;
             }
+            float w = x[0][0] + x[0][1];
+#pragma unroll
+            for (int r = 1; r < 8; ++r) w += x[r][0] + x[r][1];
             const int j = it.j0 + tid;
             if (j < T) out[(it.b * Hkv + it.hk) * T + j] = j < it.n ? w : 0.f;
         }
