@@ -123,13 +123,14 @@ constexpr int kSeedThreads = 512;
 
 // A cluster of C CTAs (1 <= C <= 8) per (b, hk) chooses the positions its cache keeps, writes
 // them, ascending, with their weights, and copies their rows. The newest `recent` are kept; of
-// the older ones the need = S - recent heaviest, found by a radix selection of the weight keys, 8
+// the older ones the need = S - recent heaviest, found by a radix selection of the weight keys, 11
 // bits a pass: the keys above the threshold, and of those equal to it the first few. Each CTA
 // counts the digits of its run of positions; the counts meet in distributed shared memory. The
 // copy, 4 D bytes read and written a slot, is the bound; the passes over 4 bytes a position come
 // before it, each with the latency of its barriers, which is why they are spread over a cluster.
-// 32 heads, 16384 positions into 2048 slots, D = 128, 70 MB: 23.5 us, about half of it the
-// selection (with C = 1, 2, 4, 8 before its passes could end early: 64, 45, 29, 26 us).
+// 32 heads, 16384 positions into 2048 slots, D = 128, 70 MB: 21.6 us, about half of it the
+// selection (with 8 bits a pass 22.7; with C = 1, 2, 4, 8 before the passes could end early 64,
+// 45, 29, 26).
 __global__ void __launch_bounds__(kSeedThreads)
     cache_seed_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                       const float* __restrict__ weights, const int64_t* __restrict__ lens, uint4* __restrict__ kc,
@@ -137,8 +138,9 @@ __global__ void __launch_bounds__(kSeedThreads)
                       int64_t vsb, int64_t vsh, int64_t vst, int Hkv, int T, int S, int recent, int vpr, int C,
                       int* status) {
     constexpr int kWarps = kSeedThreads / 32;
-    __shared__ int hist[2][256];  // of the even and the odd passes
-    __shared__ int all[256];      // the cluster's counts
+    __shared__ __align__(16) int hist[2][2048];  // of the even and the odd passes
+    __shared__ int coarse[2][256];               // of 8 digits each
+    __shared__ int all[256];                     // the cluster's coarse counts
     __shared__ int sm_a[kWarps], sm_b[kWarps];
     __shared__ int sm_cta[2];     // this CTA's keys above and equal to the threshold
     __shared__ uint32_t sm_prefix;
@@ -164,31 +166,38 @@ __global__ void __launch_bounds__(kSeedThreads)
         const int c0 = min(old, rank * run), c1 = min(old, c0 + run);
         int need = S - recent, found = 0;
         uint32_t prefix = 0, mask = 0;
-        // until the digits so far single out exactly the keys still needed (mostly after three)
-        for (int pass = 0; pass < 4 && found != need; ++pass) {
-            const int shift = 24 - 8 * pass;
+        // until the digits so far single out exactly the keys still needed (mostly after two)
+        for (int pass = 0; pass < 3 && found != need; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
             int* mine = hist[pass & 1];
-            if (tid < 256) mine[tid] = 0;
+            for (int x = tid; x < 2048; x += kSeedThreads) mine[x] = 0;
             __syncthreads();
             for (int j = c0 + tid; j < c1; j += kSeedThreads) {
                 const uint32_t key = weight_key(w[j]);
-                if ((key & mask) == prefix) atomicAdd(&mine[(key >> shift) & 255], 1);
+                if ((key & mask) == prefix) atomicAdd(&mine[(key >> shift) & ((1u << bits) - 1)], 1);
+            }
+            __syncthreads();
+            int* mine8 = coarse[pass & 1];
+            if (tid < 256) {
+                const int4 a = *reinterpret_cast<const int4*>(mine + 8 * tid), c = *reinterpret_cast<const int4*>(mine + 8 * tid + 4);
+                mine8[tid] = ((a.x + a.y) + (a.z + a.w)) + ((c.x + c.y) + (c.z + c.w));
             }
             sync();
             if (tid < 256) {
-                int sum = mine[tid];
+                int sum = mine8[tid];
                 if (C > 1) {  // the loads of all CTAs' counts in flight together
                     int x[8];
 #pragma unroll
                     for (int r = 0; r < 8; ++r)
-                        x[r] = r < C ? __float_as_int(ptx::cluster_ld(ptx::cluster_addr(&mine[tid], r))) : 0;
+                        x[r] = r < C ? __float_as_int(ptx::cluster_ld(ptx::cluster_addr(&mine8[tid], r))) : 0;
                     sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
                 }
                 all[tid] = sum;
             }
             __syncthreads();
-            if (warp == 0) {  // the digit at which the count from above reaches need
-                int own[8], sum = 0;  // lane: digits 255 - 8 lane - i
+            if (warp == 0) {
+                // the 8 digits among which the count from above reaches need ..
+                int own[8], sum = 0;  // lane: coarse digits 255 - 8 lane - i
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum += own[i] = all[255 - 8 * lane - i];
                 int incl = sum;
@@ -197,13 +206,39 @@ __global__ void __launch_bounds__(kSeedThreads)
                     const int y = __shfl_up_sync(0xffffffffu, incl, x);
                     if (lane >= x) incl += y;
                 }
-                int before = incl - sum;
-                if (before < need && need <= incl) {
+                int before = incl - sum, digit = 0;
+                const bool mine_ = before < need && need <= incl;
+                if (mine_) {
                     int i = 0;
                     while (before + own[i] < need) before += own[i++];
-                    sm_prefix = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
+                    digit = 255 - 8 * lane - i;
+                }
+                const int src = __ffs(__ballot_sync(0xffffffffu, mine_)) - 1;
+                before = __shfl_sync(0xffffffffu, before, src);
+                digit = __shfl_sync(0xffffffffu, digit, src);
+                // .. and the one of them: lane: digit 8 digit + lane % 8 of CTAs lane / 8 and 4 more
+                const int* at = mine + 8 * digit + (lane & 7);
+                int cnt = 0;
+                if (C == 1) {
+                    if (lane < 8) cnt = *at;
+                } else {
+                    const int r = lane >> 3;
+                    if (r < C) cnt = __float_as_int(ptx::cluster_ld(ptx::cluster_addr(at, r)));
+                    if (r + 4 < C) cnt += __float_as_int(ptx::cluster_ld(ptx::cluster_addr(at, r + 4)));
+                }
+                cnt += __shfl_xor_sync(0xffffffffu, cnt, 8);
+                cnt += __shfl_xor_sync(0xffffffffu, cnt, 16);
+                int upto = cnt;  // of this digit and the higher ones of the 8
+#pragma unroll
+                for (int x = 1; x < 8; x <<= 1) {
+                    const int y = __shfl_down_sync(0xffffffffu, upto, x, 8);
+                    if ((lane & 7) + x < 8) upto += y;
+                }
+                before += upto - cnt;
+                if (lane < 8 && before < need && need <= before + cnt) {
+                    sm_prefix = prefix | ((uint32_t)(8 * digit + lane) << shift);
                     sm_need = need - before;
-                    sm_found = own[i];
+                    sm_found = cnt;
                 }
             }
             __syncthreads();
