@@ -187,22 +187,24 @@ void split(int64_t units, int64_t keys, int* n, int* chunk) {
     *n = (int)((keys + c - 1) / c);
 }
 
-// Key tiles that a CTA of prefix_kernel takes, of `tiles`, when `groups` CTAs take them all: the
-// fewest rounds of 148 CTAs (one fits an SM) by the length of a round, where the start and end
-// of a CTA count as 3 tiles and a further partial state to join as half a tile.
-int prefix_chunk(int64_t groups, int tiles, int least) {
+// Key tiles that a CTA of prefix_kernel takes, of `tiles`, when `groups` CTAs take them all, on
+// `sms` SMs (one CTA fits an SM): the least time, in thousandths of a tile, of rounds of their
+// tiles and 3 for start and end, and for each partial state 0.08 and its part in the join of the
+// `rows` query rows. *time: that, in tiles.
+int prefix_chunk(int64_t groups, int tiles, int least, int64_t rows, int64_t sms, int64_t most_rounds, double* time) {
     int best = tiles;
     int64_t cost = INT64_MAX;
-    for (int ns = 1; ns <= tiles && (ns == 1 || groups * ns <= 2 * 148); ++ns) {
+    for (int ns = 1; ns <= tiles && (ns == 1 || groups * ns <= most_rounds * sms); ++ns) {
         int chunk = (tiles + ns - 1) / ns;
         if (chunk < least) chunk = least;
         const int splits = (tiles + chunk - 1) / chunk;
-        const int64_t c = (groups * splits + 147) / 148 * 2 * (chunk + 3) + splits;
+        const int64_t c = (groups * splits + sms - 1) / sms * 1000 * (chunk + 3) + splits * (80 + rows * 80 / 1000);
         if (c < cost) {
             cost = c;
             best = chunk;
         }
     }
+    *time = cost / 1000.0;
     return best;
 }
 
@@ -248,20 +250,32 @@ Plan plan(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D, bo
         }
     }
     if (p.C == 0) split(units * ((G + Q - 1) / Q), S, &p.ns, &p.chunk);
-    int64_t prefix_ctas = 0;
     if (P > p.P0) {
         p.pair = B * G > 128;
-        const int tiles = (int)((P + 127) / 128);
+        const int tiles = (int)((P + 127) / 128), least = p.pair ? 1 : 2;
         const int64_t groups = Hkv * (p.pair ? (B * G + 255) / 256 : 1);
-        p.pchunk = prefix_chunk(groups, tiles, p.pair ? 1 : 2);
+        double before;
+        p.pchunk = prefix_chunk(groups, tiles, least, B * H, 148, 2, &before);
+        // Beside stream_kernel instead, on the SMs that its CTAs leave when all of them run at once, if
+        // that is shorter (in tiles: 1.9 us, 12 MB of keys and values). 24 streams of 32 heads, 4 to a
+        // key head, P 2000, S 1000 (384 CTAs): 23.9 us with 32 CTAs beside it, 31.9 with 64 before
+        // it. It must not need the prefix's SMs: one that has run prefix_kernel keeps its shared-memory
+        // split, with too little L1 for many loads in flight, until it is idle (the same with 64
+        // CTAs beside it, which leave room for 336: 41.8 us).
+        if (p.C > 0) {
+            const int64_t per_sm = D == 128 ? 4 : 6, left = 148 - (units * p.C + per_sm - 1) / per_sm;
+            if (left >= groups) {
+                double beside;
+                const int chunk = prefix_chunk(groups, tiles, least, B * H, left, 1, &beside);
+                const double slots = units * S * D * 4 / 12e6, both = slots + Hkv * P * D * 4 / 12e6;
+                if ((beside > both ? beside : both) < before + slots) {
+                    p.pchunk = chunk;
+                    p.early = true;
+                }
+            }
+        }
         p.np = (tiles + p.pchunk - 1) / p.pchunk;
-        prefix_ctas = groups * p.np;
     }
-    // Beside the prefix's kernel when that leaves half of the SMs free (24 streams of 32 heads, 4 to a
-    // key head, S 1000, P 2000, 64 CTAs: 26.0 us, 36.4 one after the other). An SM that has run it
-    // keeps its shared-memory split, with too little L1 for many loads in flight, until it is idle
-    // (64 streams, S 1024, P 8192, 128 CTAs: 224 us, 201 one after the other).
-    p.early = p.C > 0 && p.np > 0 && prefix_ctas <= 74;
     p.NS = p.ns + p.np;
     p.off_o = round256(B * H * p.NS * 8);
     p.off_scores = p.off_o + round256(B * H * p.NS * D * 4);

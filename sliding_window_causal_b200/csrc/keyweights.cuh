@@ -461,14 +461,16 @@ __global__ void __launch_bounds__(kKwThreads, 2)
                         kw_sum16<false>(v[x & 1], nl + 16 * x, c2, 0, acc);
                     }
                 } else {
+                    // only the 16 columns that one of the warp's keys is seen by
 #pragma unroll 1
                     for (int x = 0; x < (two ? 8 : 4); ++x) {
+                        const int c0 = (x < 4 ? i0 : i1) + 16 * (x & 3);  // the query of the first column
+                        const int lo = min(max(jk - c0, 0), 16), hi = min(max(see - c0 + 1, lo), 16);
+                        if (!__any_sync(0xffffffffu, hi > lo)) continue;
                         uint32_t v[16];
                         ptx::tmem_ld16(col + 16 * x, v);
                         ptx::tmem_ld_wait();
                         ptx::reg_fence(v);
-                        const int c0 = (x < 4 ? i0 : i1) + 16 * (x & 3);  // the query of the first column
-                        const int lo = min(max(jk - c0, 0), 16), hi = min(max(see - c0 + 1, lo), 16);
                         kw_sum16<true>(v, nl + 16 * x, c2, (1u << hi) - (1u << lo), acc);
                     }
                     ptx::tc_fence_before();
