@@ -342,10 +342,10 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_ke
         const float2 e0 = lane < a.NS ? __ldcg(ml + lane) : make_float2(-INFINITY, 0.f);
         const bool writes = i % C == rank;  // the output row
         constexpr int E = D / 32;           // its columns E lane ..
-        float v[8][E];                      // the prefix's first eight states, on their way meanwhile
+        float v[16][E];                     // the prefix's first states, on their way meanwhile
         auto fetch = [&](int s0) {
 #pragma unroll
-            for (int y = 0; y < 8; ++y)
+            for (int y = 0; y < 16; ++y)
                 if (s0 + y < a.NS) ldcg_vec(a.o + (row * a.NS + s0 + y) * D + E * lane, v[y]);
         };
         if (writes) fetch(0);
@@ -366,10 +366,10 @@ __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) stream_ke
         float acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        for (int s0 = 0; s0 < a.NS; s0 += 8) {
+        for (int s0 = 0; s0 < a.NS; s0 += 16) {
             if (s0 > 0) fetch(s0);
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
+            for (int y = 0; y < 16; ++y) {
                 if (s0 + y >= a.NS) break;
                 const int s = s0 + y;
                 float f = __shfl_sync(0xffffffffu, f0, s & 31);

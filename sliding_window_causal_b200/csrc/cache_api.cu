@@ -213,10 +213,14 @@ int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 // A prefix of at most this many bytes, taken once for each stream, is left to stream_kernel: the
 // streams read it from L2, which costs less than a launch of its own and a join. 8 key heads,
 // slots 200, D = 128, own and not: 16 streams P 300 (20 MB) 9.8 and 11.1 us, 32 streams (39 MB)
-// 12.8 and 11.6, 16 streams P 1000 (66 MB) 14.6 and 11.4. Where a key head has at most 8 rows,
-// prefix_kernel's tiles are nearly empty: 2 streams P 4000 (66 MB) 13.2 and 20.1, 8 streams P
-// 4000 (131 MB) 21.2 and 21.8.
-constexpr int64_t kOwnPrefixBytes = 24 << 20, kOwnPrefixBytesFewRows = 128 << 20;
+// 12.8 and 11.6, 16 streams P 1000 (66 MB) 14.6 and 11.4. Above 128 rows a key head, where the
+// streams' query heads share what they read and prefix_kernel has twice the rows to start with, 109
+// streams of 5 key heads, P 206 (57 MB) 12.3 and 22.4. With at most 8 rows, where prefix_kernel's
+// tiles are nearly empty, 2 streams P 4000 (66 MB) 13.2 and 20.1, 8 streams P 4000 (131 MB) 21.2
+// and 21.8.
+constexpr int64_t own_prefix_bytes(int64_t rows) {
+    return (rows <= swa::kAttendQueries ? 128 : rows <= 128 ? 24 : 64) << 20;
+}
 // Scores that a CTA of stream_kernel keeps in shared memory, in bytes.
 constexpr int64_t kClusterScores = 28 << 10;
 
@@ -224,7 +228,7 @@ Plan plan(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D, bo
     Plan p = {};
     const int64_t G = H / Hkv, Q = swa::kAttendQueries, units = B * Hkv;
     if (G <= Q) {
-        const bool own = P > 0 && (B == 1 || units * P <= (B * G <= Q ? kOwnPrefixBytesFewRows : kOwnPrefixBytes) / (4 * D));
+        const bool own = P > 0 && (B == 1 || units * P <= own_prefix_bytes(B * G) / (4 * D));
         // The time of a call in the keys that a CTA takes meanwhile, by the measured rates of the
         // listed sizes: rounds of resident CTAs (4 an SM for D = 128, 6 for 64; a round that is
         // not full still takes 0.55 of its time, as its CTAs share the bandwidth among fewer), each

@@ -8,8 +8,8 @@
 // key_weights_simt_kernel (fp32): FMA on 64-key x 64-query score tiles. A CTA, or a cluster that
 // splits the query tiles, owns 64 keys, so every sum has one owner and a fixed order. Small
 // calls are bound by the latency of a tile's loads (2 streams, 4 heads, 777 tokens, D 80, W 200:
-// 28 us; 2 heads of 2000 tokens, W 2000: 54 us with clusters of 8, 213 without), large ones by
-// instruction issue (16 heads of 2000 tokens, D 64, W 1000, 3 GFLOP of multiply-adds: 174 us).
+// 24 us; 2 heads of 2000 tokens, W 2000: 54 us with clusters of 8, 213 without), large ones by
+// instruction issue (16 heads of 2000 tokens, D 64, W 1000, 3 GFLOP of multiply-adds: 160 us).
 #pragma once
 #include <cuda_bf16.h>
 #include <math.h>
@@ -27,7 +27,7 @@ constexpr int kKwTile = 64;   // keys and queries of a score tile
 constexpr int kKwDepth = 32;  // head columns staged at a time
 constexpr int kKwSimtThreads = 128;
 
-__global__ void __launch_bounds__(kKwSimtThreads, 4)
+__global__ void __launch_bounds__(kKwSimtThreads, 3)
     key_weights_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ lse,
                             const int64_t* __restrict__ lens, float* __restrict__ out, int64_t qsb, int64_t qsh,
                             int64_t qst, int64_t ksb, int64_t ksh, int64_t kst, int H, int Hkv, int T, int D, int W,
@@ -100,16 +100,19 @@ __global__ void __launch_bounds__(kKwSimtThreads, 4)
                 settle();
                 if (gh < G) fetch(0);
             }
-#pragma unroll 8
-            for (int d = 0; d < kKwDepth; ++d) {
-                const float4 x = *reinterpret_cast<const float4*>(&sq[chunk][d][4 * tq]);
-                const float4 y = *reinterpret_cast<const float4*>(&sk[chunk][d][8 * tk]);
-                const float4 z = *reinterpret_cast<const float4*>(&sk[chunk][d][8 * tk + 4]);
-                const float xs[4] = {x.x, x.y, x.z, x.w}, ys[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+            const int dn = min(kKwDepth, D - d0);  // in steps of 8: the columns past D hold zeros
+            for (int d8 = 0; d8 < dn; d8 += 8) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int d = d8; d < d8 + 8; ++d) {
+                    const float4 x = *reinterpret_cast<const float4*>(&sq[chunk][d][4 * tq]);
+                    const float4 y = *reinterpret_cast<const float4*>(&sk[chunk][d][8 * tk]);
+                    const float4 z = *reinterpret_cast<const float4*>(&sk[chunk][d][8 * tk + 4]);
+                    const float xs[4] = {x.x, x.y, x.z, x.w}, ys[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) c[e][f] = fmaf(ys[e], xs[f], c[e][f]);
+                    for (int e = 0; e < 8; ++e)
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) c[e][f] = fmaf(ys[e], xs[f], c[e][f]);
+                }
             }
         }
         const float4 l4 = *reinterpret_cast<const float4*>(&sl[ltile][4 * tq]);
