@@ -303,6 +303,7 @@ DECODE_CASES = [
     # prefixes too long for each stream to read by itself
     (24, 2, 4, 128, 50, 1100), (60, 2, 2, 64, 70, 2100), (100, 2, 3, 64, 33, 700), (16, 1, 8, 128, 40, 4000),
     (2, 1, 1, 128, 30, 140000), (3, 2, 12, 64, 500, 5000), (9, 1, 1, 64, 100, 40001), (40, 8, 1, 128, 600, 300),
+    (100, 2, 3, 64, 33, 1500), (70, 1, 7, 128, 900, 2500), (200, 2, 2, 64, 1, 3000),
 ]
 
 
@@ -341,7 +342,7 @@ def test_decode_never_reads_slots_without_a_token(G):
     swa.device_status()
 
 
-@pytest.mark.parametrize("B,G,P", [(2, 1, 200), (40, 4, 200), (40, 4, 1000), (20, 4, 2000)])
+@pytest.mark.parametrize("B,G,P", [(2, 1, 200), (40, 4, 200), (40, 4, 1000), (20, 4, 2000), (40, 4, 2500)])
 def test_decode_reads_a_strided_prefix_and_nothing_past_it(B, G, P):
     """A prefix that is a slice of a longer [P,Hkv,D] buffer whose other rows hold NaN."""
     Hkv, D, S = 3, 64, 20
@@ -355,7 +356,7 @@ def test_decode_reads_a_strided_prefix_and_nothing_past_it(B, G, P):
     assert torch.equal(out, swa.prefix_decode(q, kp.contiguous(), vp.contiguous(), kc, vc, pos, S))
 
 
-@pytest.mark.parametrize("B,G,P", [(1, 1, 300), (3, 8, 500), (80, 2, 700), (80, 2, 2000), (40, 2, 4000)])
+@pytest.mark.parametrize("B,G,P", [(1, 1, 300), (3, 8, 500), (80, 2, 700), (80, 2, 2000), (40, 2, 4000), (80, 2, 4000)])
 def test_decode_of_sharp_and_growing_scores(B, G, P):
     """Scores that grow along the keys by hundreds, so that every running maximum is replaced
     many times, and rows where one key far outweighs the rest."""
