@@ -435,12 +435,13 @@ __global__ void __launch_bounds__(kKwThreads, 2)
                 }
                 continue;
             }
-            ptx::f32x2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+            float mine = 0.f;  // by way of each stage's own sum: fewer additions to the large one
             for (int j = first; j < stages; j += 2) {
                 const uint32_t Jj = J + j;
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full + y, (Jj >> 1) & 1, wait_limit_ns, abort_flag));
                 if (!ok) break;
                 ptx::tc_fence_after();
+                ptx::f32x2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
                 const int at1 = at + 1 < per_head ? at + 1 : 0;
                 const int i0 = i_lo + kKwSlice * at, i1 = i_lo + kKwSlice * at1;
                 const bool two = slices - 2 * j >= 2;
@@ -480,11 +481,11 @@ __global__ void __launch_bounds__(kKwThreads, 2)
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(s_read + y);
                 }
+                mine += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
                 at += 4;
                 while (at >= per_head) at -= per_head;
             }
             if (!ok) break;
-            const float mine = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
             if (C > 1) {
                 sm_red[128 * y + row] = mine;
             } else {
