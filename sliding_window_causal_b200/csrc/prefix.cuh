@@ -1,7 +1,8 @@
 // prefix.cuh: the queries of a whole batch over a prefix that they share, bf16, D = 64/128, on
 // the tensor cores. Row r of key head hk is query head hk G + r % G of stream r / G; every row
 // sees every prefix key, so this is a dense attention of B G rows a key head whose softmax is
-// taken in splits of the keys and joined by finish_kernel (attend.cuh): each split writes
+// taken in splits of the keys and joined by stream_kernel or finish_kernel (attend.cuh): each
+// split writes
 //   m, l = sum_j 2^(z_j - m), o = sum_j 2^(z_j - m) v_j,   z = scale log2(e) q.k.
 //
 // prefix_kernel<D, PAIR>: CTA = (key head, group of rows, split of the key tiles), two lanes of
@@ -9,13 +10,13 @@
 // of TMEM and its softmax warpgroup:
 //   PAIR   (more than 128 rows a key head) lane x has row tile x and takes every key tile, so
 //          that a key tile in shared memory serves 256 rows;
-//   !PAIR  (fewer) both lanes have the one row tile and take every second key tile, and join at the end:
-//          with up to 128 rows the prefix's bytes bound the call, and one lane's chain
+//   !PAIR  (fewer) both lanes have the one row tile and take every second key tile, and join at
+//          the end: with up to 128 rows the prefix's bytes bound the call, and one lane's chain
 //          S -> softmax -> P V would be too slow to ask for them.
 // While one lane is in its softmax the tensor core works for the other. Roles: warp 0 TMA
 // producer (K and V tiles through one ring), warp 1 MMA issuer, warps 4 .. 7 and 8 .. 11 the
-// softmax of lanes 0 and 1 (prefix_tile, a row a thread). Q goes to shared memory by plain loads, in the layout of a
-// TMA tile, since G query heads of 128 / G streams are no box for every G.
+// softmax of lanes 0 and 1 (prefix_tile, a row a thread). Q goes to shared memory by plain loads,
+// in the layout of a TMA tile, since G query heads of 128 / G streams are no box for every G.
 //
 // Measured, D = 128: 128 streams of 32 heads, 4 to a key head, behind 65536 keys (PAIR, 137 GFLOP):
 // 0.118 ms, 1.16 PFLOP/s; hi + lo parts there 0.148 ms, P handed over in 1 or 4 parts instead of 2
