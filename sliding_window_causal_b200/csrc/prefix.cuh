@@ -23,9 +23,13 @@
 // 0.125 and 0.122 ms. 64 streams of 32 heads (!PAIR): 72 us more for 24576 more keys, 5.6 TB/s.
 //
 // P is rounded to bf16. !PAIR carries it as hi + lo parts (2^-16), for the second product costs
-// nothing there. PAIR is bound by tensor core and exponentials and carries one part: each weight
-// is off by up to 2^-8 of itself, which in the output is at most as much as the rounding of the
-// output that follows. The row sums take the fp32 weights either way.
+// nothing there. PAIR is bound by tensor core and exponentials: a warp carries two parts only of a
+// tile in which a key of one of its rows weighs more than a third of what the row has met before
+// (so it could end up above a quarter), and one part of the others, each weight off by up to 2^-8
+// of itself. So that the error of a key that weighs much cancels, o is divided by the sum of the
+// weights as the products took them: it is scaled by l / l', with l' that sum, and (m, l) stay
+// those of the fp32 weights, from which the slots' own weights grow. What is left is at most 2^-8
+// sum p |v - o| over the keys of one part.
 #pragma once
 #include <cuda_bf16.h>
 #include <math.h>
@@ -52,22 +56,59 @@ struct PrefixCfg {
     // q_full, ring_full[S], ring_empty[S], s_full[2], p_full[2][kPPParts], o_final[2], drain
     static constexpr int kNumBars = 1 + 2 * kStages + 2 + 2 * kPPParts + 2 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-    static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
+    static constexpr int kLoOff = (kMiscOff + 8 + 15) & ~15;  // low-part flags [2 lanes][2 parities][4 warps]
+    static constexpr int kSmemBytes = kLoOff + 64 + 1024;
     static constexpr uint32_t kTmemCols = 512;
     __device__ static constexpr uint32_t colS(int x) { return 128u * x; }
     __device__ static constexpr uint32_t colO(int x) { return 256u + 128u * x; }
 };
 
-// One tile of one row: the thread's 128 scores at TMEM column scol become P = 2^(z - m), z = s c
-// (c = scale_log2), in place as bf16 pairs: keys 32k .. 32k+31 in columns 32k .. 32k+15 and, with
-// LO, the rest p - bf16(p), again bf16, in columns 32k+16 .. 32k+31. TAIL: only columns 0 .. last
-// are keys. m is the row's reference (-inf before its first tile): a row whose maximum passes it
-// by more than 2^8 moves it up by a whole power of two, which rescales O (at ocol) and l exactly.
-// l grows by the fp32 weights, not the rounded ones. after_part(p): part p of P is stored, with
-// one more chunk's arithmetic behind it.
-template <int D, bool TAIL, bool LO, typename AfterPart>
-__device__ __forceinline__ void prefix_tile(uint32_t scol, uint32_t ocol, float scale_log2, float& m, float& l, int last,
-                                            AfterPart after_part) {
+// P = 2^(s c - mu) of the thread's 128 scores v (c = scale_log2), over S at TMEM column scol as bf16
+// pairs: keys 32k .. 32k+31 in columns 32k .. 32k+15 and, with LO, the rest p - bf16(p), again
+// bf16, in columns 32k+16 .. 32k+31. after_part(p): part p of P is stored, with one more chunk's
+// arithmetic behind it. l grows by the fp32 weights, lw by the weights as written (with LO they
+// are the same to 2^-17).
+template <bool LO, typename AfterPart>
+__device__ __forceinline__ void prefix_exps(uint32_t scol, const uint32_t (&v)[4][32], float scale_log2, float mu, float& l,
+                                            float& lw, AfterPart after_part) {
+    const ptx::f32x2 sc = {scale_log2, scale_log2}, nm = {-mu, -mu};
+    ptx::f32x2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+    ptx::f32x2 accw[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t ph[16], pl[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            const ptx::f32x2 z = ptx::fma2({__uint_as_float(v[c][2 * t]), __uint_as_float(v[c][2 * t + 1])}, sc, nm);
+            const ptx::f32x2 e = {ptx::ex2(z.x), ptx::ex2(z.y)};
+            acc[t & 3] = ptx::add2(acc[t & 3], e);
+            ph[t] = ptx::pack_bf16x2(e.x, e.y);
+            if (LO) {
+                const ptx::f32x2 r = ptx::sub2(e, {ptx::bf16lo_f32(ph[t]), ptx::bf16hi_f32(ph[t])});
+                pl[t] = ptx::pack_bf16x2(r.x, r.y);
+            } else {
+                accw[t & 3] = ptx::add_bf16x2_f32(ph[t], accw[t & 3]);
+            }
+        }
+        if (c > 0 && c % (4 / kPPParts) == 0) after_part(c / (4 / kPPParts) - 1);
+        ptx::tmem_st16(scol + 32 * c, ph);
+        if (LO) ptx::tmem_st16(scol + 32 * c + 16, pl);
+    }
+    after_part(kPPParts - 1);
+    const float e = ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) + ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y));
+    l += e;
+    if (LO) lw += e;
+    else lw += ((accw[0].x + accw[0].y) + (accw[1].x + accw[1].y)) + ((accw[2].x + accw[2].y) + (accw[3].x + accw[3].y));
+}
+
+// One tile of one row: the thread's 128 scores at TMEM column scol become P in place, relative to
+// m, the row's reference (-inf before its first tile): a row whose maximum passes it by more than
+// 2^8 moves it up by a whole power of two, which rescales O (at ocol), l and lw exactly. TAIL:
+// only columns 0 .. last are keys. ADAPT: the warp chooses whether P has low parts, and
+// publish(bool) says so before the first part is handed over; else it always has.
+template <int D, bool TAIL, bool ADAPT, typename AfterPart, typename Publish>
+__device__ __forceinline__ void prefix_tile(uint32_t scol, uint32_t ocol, float scale_log2, float& m, float& l, float& lw,
+                                            int last, AfterPart after_part, Publish publish) {
     uint32_t v[4][32];
 #pragma unroll
     for (int c = 0; c < 4; ++c) ptx::tmem_ld32(scol + 32 * c, v[c]);
@@ -100,32 +141,19 @@ __device__ __forceinline__ void prefix_tile(uint32_t scol, uint32_t ocol, float 
         __syncwarp();
         pp_rescale<D, false>(ocol, scol, 0, f);
         l *= f;
+        lw *= f;
         m += (float)k;
     }
     if (m == -INFINITY) m = tm;
     const float mu = m == -INFINITY ? 0.f : m;
-    const ptx::f32x2 sc = {scale_log2, scale_log2}, nm = {-mu, -mu};
-    ptx::f32x2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t ph[16], pl[16];
-#pragma unroll
-        for (int t = 0; t < 16; ++t) {
-            const ptx::f32x2 z = ptx::fma2({__uint_as_float(v[c][2 * t]), __uint_as_float(v[c][2 * t + 1])}, sc, nm);
-            const ptx::f32x2 e = {ptx::ex2(z.x), ptx::ex2(z.y)};
-            acc[t & 3] = ptx::add2(acc[t & 3], e);
-            ph[t] = ptx::pack_bf16x2(e.x, e.y);
-            if (LO) {
-                const ptx::f32x2 r = ptx::sub2(e, {ptx::bf16lo_f32(ph[t]), ptx::bf16hi_f32(ph[t])});
-                pl[t] = ptx::pack_bf16x2(r.x, r.y);
-            }
-        }
-        if (c > 0 && c % (4 / kPPParts) == 0) after_part(c / (4 / kPPParts) - 1);
-        ptx::tmem_st16(scol + 32 * c, ph);
-        if (LO) ptx::tmem_st16(scol + 32 * c + 16, pl);
+    if constexpr (ADAPT) {
+        const bool lo = __any_sync(0xffffffffu, tm != -INFINITY && 3.f * ptx::ex2(tm - mu) > l);
+        publish(lo);
+        if (lo) prefix_exps<true>(scol, v, scale_log2, mu, l, lw, after_part);
+        else prefix_exps<false>(scol, v, scale_log2, mu, l, lw, after_part);
+    } else {
+        prefix_exps<true>(scol, v, scale_log2, mu, l, lw, after_part);
     }
-    after_part(kPPParts - 1);
-    l += ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) + ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y));
 }
 
 // a: q, ml, o, B, H, Hkv, G, S (prefix length), chunk (key tiles a split takes), NS, scale_log2
@@ -136,7 +164,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                   uint64_t wait_limit_ns) {
     using Cf = PrefixCfg<D, PAIR>;
     constexpr int NS = Cf::kStages;
-    constexpr bool LO = !PAIR;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + Cf::kBarOff);
@@ -148,6 +175,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     uint64_t* drain = o_final + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cf::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cf::kMiscOff + 4);
+    // [4 (2x + parity) + w]: warp w of lane x wrote low parts of P for the tile of that parity
+    volatile uint32_t* lo_flag = reinterpret_cast<volatile uint32_t*>(smem + Cf::kLoOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     const int n_rows = a.B * a.G;
@@ -248,19 +277,31 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             };
             auto issue_pv = [&](int x, uint32_t L, int j) {  // O_x (+)= P_x V as the parts of P arrive
                 const uint32_t v_lo = (ring_lo + L % NS * kTileLo) | lo_v;
+                bool some = true;  // some warp of the lane wrote low parts; dis: the rows of those that did not
+                uint32_t dis[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
                 for (int part = 0; part < kPPParts; ++part) {
                     if (ok) ok = pp_wait_warp(p_full + kPPParts * x + part, j & 1, wait_limit_ns, abort_flag);
                     if (!ok) return;
                     ptx::tc_fence_after();
                     constexpr int kPer = 8 / kPPParts;
+                    const uint32_t p_col = tmem + Cf::colS(x), o_col = tmem + Cf::colO(x);
 #pragma unroll
-                    for (int lo = 0; lo < (LO ? 2 : 1); ++lo)
+                    for (int kk = part * kPer; kk < (part + 1) * kPer; ++kk)
+                        ptx::mma_ts_one(o_col, p_col + pp_pcol(kk), desc_hi | (v_lo + kk * (2048 >> 4)), idesc_o,
+                                        (j > 0 || kk > 0) ? 1u : 0u);
+                    if (PAIR && part == 0) some = pp_lo_lanes(lo_flag, x, j, dis);
+                    if (PAIR && some && (dis[0] | dis[1] | dis[2] | dis[3]) != 0u) {
 #pragma unroll
                         for (int kk = part * kPer; kk < (part + 1) * kPer; ++kk)
-                            ptx::mma_ts_one(tmem + Cf::colO(x), tmem + Cf::colS(x) + pp_pcol(kk) + 16 * lo,
-                                            desc_hi | (v_lo + kk * (2048 >> 4)), idesc_o,
-                                            (j > 0 || kk > 0 || lo > 0) ? 1u : 0u);
+                            ptx::mma_ts_one_masked(o_col, p_col + pp_pcol(kk) + 16, desc_hi | (v_lo + kk * (2048 >> 4)),
+                                                   idesc_o, 1u, dis);
+                    } else if (some) {
+#pragma unroll
+                        for (int kk = part * kPer; kk < (part + 1) * kPer; ++kk)
+                            ptx::mma_ts_one(o_col, p_col + pp_pcol(kk) + 16, desc_hi | (v_lo + kk * (2048 >> 4)),
+                                            idesc_o, 1u);
+                    }
                 }
             };
             if (PAIR) {
@@ -337,7 +378,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t scol = tl + Cf::colS(x), ocol = tl + Cf::colO(x);
         const int mine = PAIR ? n : (n + 1 - x) / 2;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, lw = 0.f;
         bool ok = true;
         // S_x(j) follows P_x(j-1) V in the tensor core's order: once S_x(j) is there, O_x is at rest
         auto after_part = [&](int part) {
@@ -347,18 +388,22 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             if (lane == 0) ptx::mbar_arrive(p_full + kPPParts * x + part);
         };
         for (int j = 0; j < mine; ++j) {
+            auto publish = [&](bool lo) {
+                if (lane == 0) lo_flag[4 * (2 * x + (j & 1)) + quarter] = lo ? 1u : 0u;
+            };
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full + x, j & 1, wait_limit_ns, abort_flag));
             if (!ok) break;
             ptx::tc_fence_after();
             const int last = a.S - 1 - 128 * (t0 + (PAIR ? j : 2 * j + x));  // last key of the tile
-            if (last >= 127) prefix_tile<D, false, LO>(scol, ocol, a.scale_log2, m, l, 127, after_part);
-            else prefix_tile<D, true, LO>(scol, ocol, a.scale_log2, m, l, last, after_part);
+            if (last >= 127) prefix_tile<D, false, PAIR>(scol, ocol, a.scale_log2, m, l, lw, 127, after_part, publish);
+            else prefix_tile<D, true, PAIR>(scol, ocol, a.scale_log2, m, l, lw, last, after_part, publish);
         }
         const int64_t at = qrow * a.NS + (int)blockIdx.y;
         if (PAIR) {
             if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(o_final + x, 0, wait_limit_ns, abort_flag));
             if (ok) {
                 ptx::tc_fence_after();
+                const float f = lw > 0.f ? l / lw : 1.f;  // neither is where every score is NaN or -inf
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -369,8 +414,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                         float4* to = reinterpret_cast<float4*>(a.o + at * D + 32 * c);
 #pragma unroll
                         for (int t = 0; t < 8; ++t)
-                            to[t] = make_float4(__uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]),
-                                                __uint_as_float(o[4 * t + 2]), __uint_as_float(o[4 * t + 3]));
+                            to[t] = make_float4(__uint_as_float(o[4 * t]) * f, __uint_as_float(o[4 * t + 1]) * f,
+                                                __uint_as_float(o[4 * t + 2]) * f, __uint_as_float(o[4 * t + 3]) * f);
                     }
                 }
             }

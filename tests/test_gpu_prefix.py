@@ -1,0 +1,68 @@
+"""The shared prefix's kernel where a whole batch's rows are 129 and more to a key head (two row
+tiles a CTA) and where a CTA takes many key tiles: rows that few keys dominate, every key once,
+reference values that move far. Bounds are roundings counted, none fitted."""
+import math
+
+import pytest
+import torch
+
+import serving_ref as ref
+import sliding_window_causal_b200 as swa
+from test_gpu_serving import DEV, gen, heavy, rand
+
+pytestmark = pytest.mark.gpu
+
+
+def exact_rows(q, kc, vc, pos, kp, vp):
+    """(out, centred, spread, gain, ez) in float64: out, the sums of p |v - out| and of p |v|, the
+    weight that each slot gets, and how far fp32 scores may move an exponent."""
+    B, H, D = q.shape
+    Hkv, S = kc.shape[1], kc.shape[2]
+    G, c = H // Hkv, 1 / math.sqrt(D)
+    out, centred, spread = (torch.zeros(B, H, D, dtype=torch.float64, device=DEV) for _ in range(3))
+    gain = torch.zeros(B, Hkv, S, dtype=torch.float64, device=DEV)
+    ez = 0.0
+    for b in range(B):
+        n = min(int(pos[b]) + 1, S)
+        for hk in range(Hkv):
+            ks, vs = (torch.cat([p[hk], r[b, hk, :n]]).double() for p, r in ((kp, kc), (vp, vc)))
+            qd = q[b, hk * G:(hk + 1) * G].double()
+            p = torch.softmax(c * (qd @ ks.T), 1)
+            o = p @ vs
+            out[b, hk * G:(hk + 1) * G] = o
+            spread[b, hk * G:(hk + 1) * G] = p @ vs.abs()
+            gain[b, hk, :n] = p[:, -n:].sum(0)
+            for x in range(G):
+                centred[b, hk * G + x] = p[x] @ (vs - o[x]).abs()
+            ez = max(ez, (D + 4) * ref.U32 * c * float((qd.abs() @ ks.abs().T).max()))
+    return out, centred, spread, gain, ez
+
+
+@pytest.mark.parametrize("B,Hkv,G,D,S,P,scale", [
+    (100, 2, 3, 64, 33, 1500, 4), (40, 2, 4, 128, 20, 4000, 8), (48, 1, 4, 128, 9, 9000, 8), (200, 2, 2, 64, 1, 3000, 8),
+    (129, 1, 1, 128, 5, 3300, 16)])
+def test_rows_that_few_keys_dominate(B, Hkv, G, D, S, P, scale):
+    """Queries scaled up, so that one or a few keys hold most of a row's weight. A weight rounded
+    to bf16 is off by at most 2^-8 of itself, in the product and in the sum that the output is
+    divided by, so of a split's output o it moves sum p e (v - o), at most 2^-8 sum p |v - o|
+    over the split (1 + 2^-7 for the divisor). The distance to the split's own mean is at most
+    twice that to any other point, here the whole row's output."""
+    g = gen(B + P + scale)
+    q = rand(g, B, Hkv * G, D, scale=float(scale))
+    kc, vc, kp, vp = rand(g, B, Hkv, S, D), rand(g, B, Hkv, S, D), rand(g, Hkv, P, D), rand(g, Hkv, P, D)
+    pos = torch.randint(0, 2 * S, (B,), generator=g, device=DEV)
+    want, centred, spread, gain, ez = exact_rows(q, kc, vc, pos, kp, vp)
+    fine = 2 * ez + 2.0 ** -20 + 2.0 ** -15 + 2 * (P + S) * ref.U32  # exponents, hi + lo parts, sums in fp32
+    tol = ref.UBF * want.abs() + (1 + ref.UBF) * (2 * ref.UBF * (1 + 2.0 ** -7) * centred + fine * spread)
+    before = heavy(g, B, Hkv, S)
+    after = before.clone()
+    for out in (swa.prefix_decode(q, kp, vp, kc, vc, pos, S), swa.cache_decode(q, kc, vc, after, pos, kp, vp)):
+        off = (out.double() - want).abs()
+        assert bool((off <= tol).all()), float((off / tol).max())
+        assert float(off[want.abs() < 4].max()) <= 1e-2  # as the prefill, below the coarser steps of bf16
+    swa.device_status()
+    # The slots' weights keep the fp32 sums: exponents and sums as in test_gpu_serving, and each of
+    # the G probabilities below fp32's normal numbers may be taken as 0, so 2^-126 each.
+    tol = ref.U32 * (before.double() + gain) * 2 + gain * (2 * ez + 2.0 ** -20 + (P + S + G) * ref.U32) + G * 2.0 ** -126
+    off = (after.double() - (before.double() + gain)).abs()
+    assert bool((off <= tol).all()), float((off - tol).max())
