@@ -135,14 +135,16 @@ __device__ __forceinline__ void prefix_tile(uint32_t scol, uint32_t ocol, float 
     const float tm = ptx::max3(ptx::max3(q[0], q[1], q[2]), ptx::max3(q[3], q[4], q[5]), fmaxf(q[6], q[7])) * scale_log2;
     const bool need = m != -INFINITY && tm > m + kPPRescaleThreshold;
     if (__any_sync(0xffffffffu, need)) {
-        // in full, so that no weight of this tile exceeds 1; beyond 2^-126 the old sums vanish
-        const int k = need ? (int)fminf(ceilf(tm - m), 1048576.0f) : 0;
-        const float f = k > 126 ? 0.f : pp_pow2_neg(k);
+        // in full, so that no weight of this tile exceeds 1; beyond 2^-126 the old sums vanish and
+        // the tile's maximum itself is the reference
+        const float up = need ? ceilf(tm - m) : 0.f;
+        const bool gone = up > 126.f;
+        const float f = gone ? 0.f : pp_pow2_neg((int)up);
         __syncwarp();
         pp_rescale<D, false>(ocol, scol, 0, f);
         l *= f;
         lw *= f;
-        m += (float)k;
+        m = gone ? tm : m + up;
     }
     if (m == -INFINITY) m = tm;
     const float mu = m == -INFINITY ? 0.f : m;

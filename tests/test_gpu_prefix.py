@@ -8,7 +8,7 @@ import torch
 
 import serving_ref as ref
 import sliding_window_causal_b200 as swa
-from test_gpu_serving import DEV, gen, heavy, rand
+from test_gpu_serving import BF, DEV, gen, heavy, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,34 @@ def test_rows_that_few_keys_dominate(B, Hkv, G, D, S, P, scale):
     tol = ref.U32 * (before.double() + gain) * 2 + gain * (2 * ez + 2.0 ** -20 + (P + S + G) * ref.U32) + G * 2.0 ** -126
     off = (after.double() - (before.double() + gain)).abs()
     assert bool((off <= tol).all()), float((off - tol).max())
+
+
+@pytest.mark.parametrize("B,Hkv,G,D,S,P", [
+    (200, 2, 2, 64, 5, 3000), (40, 2, 4, 128, 5, 30011),     # two row tiles a CTA: 2 and 5 key tiles each
+    (9, 1, 1, 64, 5, 40001), (2, 1, 1, 128, 5, 140000),      # one row tile, alternate key tiles on two lanes
+    (3, 1, 2, 64, 700, 100)])                                # the streams read it by themselves
+def test_scores_that_rise_beyond_every_power_of_two(B, Hkv, G, D, S, P):
+    """Scores that rise by 2^21 (powers of two) from one key tile to the next: a row's weight is
+    all on the last tile's keys, in equal shares, and nothing of the others is left or infinite.
+    Queries (1, 0, ..) and keys (tile, 0, ..) make every score exact."""
+    g = gen(P)
+    step = 2.0 ** 21 / math.log2(math.e)
+    q = torch.zeros(B, Hkv * G, D, dtype=BF, device=DEV)
+    q[..., 0] = 1
+    tile = torch.arange(P, device=DEV) // 128
+    kp = torch.zeros(Hkv, P, D, dtype=BF, device=DEV)
+    kp[..., 0] = (tile - int(tile[-1])).clamp_min(-256).to(BF)  # whole numbers that bf16 holds
+    vp, vc = rand(g, Hkv, P, D), rand(g, B, Hkv, S, D)
+    kc = torch.zeros(B, Hkv, S, D, dtype=BF, device=DEV)
+    kc[..., 0] = -1
+    pos = torch.full((B,), S, device=DEV)
+    for flip in (False, True):  # rising and falling
+        if flip:
+            kp, vp = kp.flip(1).contiguous(), vp.flip(1).contiguous()
+        top = (kp[0, :, 0] == 0).nonzero().flatten()
+        want = vp[:, top].double().mean(1)[None, :, None].expand(B, Hkv, G, D).reshape(B, Hkv * G, D)
+        out = swa.prefix_decode(q, kp, vp, kc, vc, pos, S, scale=step)
+        spread = vp[:, top].double().abs().mean(1)[None, :, None].expand(B, Hkv, G, D).reshape(B, Hkv * G, D)
+        swa.device_status()
+        tol = ref.decode_tol(want, spread, 0.0, 128, 2.0 ** -8)
+        assert bool(((out.double() - want).abs() <= tol).all())
