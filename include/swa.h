@@ -384,7 +384,7 @@ int swa_decode_noalloc(const void* q, const void* kring, const void* vring, cons
  *   lse     : [B,H,T] fp32 contiguous, as swa_forward_lse writes it for the same scale and W.
  *   weights : [B,Hkv,T] fp32 contiguous, overwritten.
  *   dtype   : SWA_BF16 (D 64 or 128, 16-byte aligned) or SWA_F32 (any D <= 4096).
- *   scale   : finite, any sign.
+ *   scale   : finite, any sign; scale * log2(e) beyond fp32 -> SWA_ERR_UNSUPPORTED.
  * Scores, exponentials and sums are fp32. A lens[b] outside [0, T] is found on the device:
  * that stream's weights are written as zeros and swa_device_status() reports
  * SWA_ERR_INVALID_ARG. Errors: as swa_forward_ex, plus last < 1 or H not a multiple of Hkv ->
@@ -445,7 +445,8 @@ int swa_cache_append(const void* k, const void* v, void* kcache, void* vcache, f
  *                      256-byte aligned (NULL if that is 0); its contents need no preparation
  *                      and mean nothing afterwards. Calls that may run at the same time need
  *                      their own.
- *   scale            : of the scores, > 0.      D : 64 or 128.
+ *   scale            : of the scores, > 0 (scale * log2(e) beyond fp32 -> SWA_ERR_UNSUPPORTED).
+ *   D                : 64 or 128.
  * Scores, statistics and sums are fp32. A negative pos[b] is found on the device: that stream's
  * output is zeros, its weights stay and swa_device_status() reports SWA_ERR_INVALID_ARG.
  * Errors: as swa_forward_ex, plus a workspace that is too short -> SWA_ERR_INVALID_ARG.

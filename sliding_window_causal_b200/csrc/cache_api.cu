@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdint>
@@ -50,6 +51,16 @@ int check_heads(const char* fn, int64_t B, int64_t H, int64_t Hkv, int64_t D) {
         return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     if (H > 0 && H / Hkv > kMaxGroup)
         return fail(SWA_ERR_UNSUPPORTED, "%s: more than %lld query heads to a key head", fn, (long long)kMaxGroup);
+    return SWA_OK;
+}
+// scale log2(e), the fp32 factor of the scores. A positive one too small for fp32 becomes the least
+// that is not 0, so that a masked score, -infinity, stays that (the scores come out as 0 all the same).
+int scale_log2(const char* fn, double scale, float* out) {
+    if (!std::isfinite(scale)) return fail(SWA_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    const double x = 1.4426950408889634 * scale;
+    if (std::fabs(x) > FLT_MAX) return fail(SWA_ERR_UNSUPPORTED, "%s: scale %g is beyond fp32", fn, scale);
+    *out = (float)x;
+    if (scale > 0.0 && *out == 0.f) *out = FLT_TRUE_MIN;
     return SWA_OK;
 }
 int check_head_dim(const char* fn, int64_t D) {
@@ -135,7 +146,7 @@ int allow_smem(const void* kernel, int bytes, int regs = 0) {
 // ------------------------------------------------------------------ key weights
 template <int D>
 int launch_key_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const float* lse, const int64_t* lens,
-                       float* weights, int64_t B, int64_t H, int64_t Hkv, int64_t T, int W, int last, double scale,
+                       float* weights, int64_t B, int64_t H, int64_t Hkv, int64_t T, int W, int last, float c2,
                        int* status, cudaStream_t s) {
     auto* kernel = swa::key_weights_tc_kernel<D>;
     if (int rc = allow_smem(reinterpret_cast<const void*>(kernel), swa::KwCfg<D>::kSmemBytes)) return rc;
@@ -160,7 +171,7 @@ int launch_key_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const f
     cudaLaunchAttribute at[1];
     cluster_of(&cfg, at, C);
     cudaLaunchKernelEx(&cfg, kernel, tm_q, tm_k, lse, lens, weights, units, (int)H, (int)Hkv, (int)T, W,
-                       last, (float)(1.4426950408889634 * scale), C, swa_internal::wait_limit_ns(), status);
+                       last, c2, C, swa_internal::wait_limit_ns(), status);
     return SWA_OK;
 }
 
@@ -371,7 +382,8 @@ int decode(const char* fn, const void* q, const void* k, const void* v, const in
            float* weights, bool scores, void* out, void* workspace, int64_t workspace_bytes, int64_t B, int64_t H,
            int64_t Hkv, int64_t S, int64_t P, int64_t D, double scale, const int64_t* strides, void* stream) {
     if (int rc = check_decode_sizes(fn, B, H, Hkv, S, P, D)) return rc;
-    if (!std::isfinite(scale)) return fail(SWA_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    float c2;
+    if (int rc = scale_log2(fn, scale, &c2)) return rc;
     if (B == 0 || H == 0) return success();
     if (!(scale > 0.0)) return fail(SWA_ERR_UNSUPPORTED, "%s: scale must be > 0 (got %g)", fn, scale);
     if (!q || !k || !v || !pos || !out || (scores && !weights) || (P > 0 && (!kp || !vp)))
@@ -415,7 +427,7 @@ int decode(const char* fn, const void* q, const void* k, const void* v, const in
     a.chunk = pl.chunk;
     a.split0 = pl.np;  // the prefix's partial states come first
     a.NS = (int)pl.NS;
-    a.scale_log2 = (float)(1.4426950408889634 * scale);
+    a.scale_log2 = c2;
     a.status = status;
     swa::AttendArgs pre = a;
     pre.k = static_cast<const __nv_bfloat16*>(kp);
@@ -455,7 +467,8 @@ int swa_key_weights(const void* q, const void* k, const float* lse, const int64_
     if (T < 0) return fail(SWA_ERR_INVALID_ARG, "%s: negative size T=%lld", fn, (long long)T);
     if (W < 1) return fail(SWA_ERR_INVALID_ARG, "%s: window W=%lld must be >= 1", fn, (long long)W);
     if (last < 1) return fail(SWA_ERR_INVALID_ARG, "%s: last=%lld must be >= 1", fn, (long long)last);
-    if (!std::isfinite(scale)) return fail(SWA_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    float c2;
+    if (int rc = scale_log2(fn, scale, &c2)) return rc;
     if (B == 0 || H == 0 || T == 0) return success();
     if (!q || !k || !lse || !weights) return fail(SWA_ERR_INVALID_ARG, "%s: null pointer", fn);
     if (dtype == SWA_BF16) {
@@ -486,8 +499,8 @@ int swa_key_weights(const void* q, const void* k, const float* lse, const int64_
         CUtensorMap tm_q, tm_k;
         if (int rc = swa_internal::tensor_map(&tm_q, q, B, H, T, D, qs, swa::kKwSlice)) return rc;
         if (int rc = swa_internal::tensor_map(&tm_k, k, B, Hkv, T, D, ks, 128)) return rc;
-        if (int rc = D == 128 ? launch_key_weights<128>(tm_q, tm_k, lse, lens, weights, B, H, Hkv, T, Wi, Li, scale, status, s)
-                              : launch_key_weights<64>(tm_q, tm_k, lse, lens, weights, B, H, Hkv, T, Wi, Li, scale, status, s))
+        if (int rc = D == 128 ? launch_key_weights<128>(tm_q, tm_k, lse, lens, weights, B, H, Hkv, T, Wi, Li, c2, status, s)
+                              : launch_key_weights<64>(tm_q, tm_k, lse, lens, weights, B, H, Hkv, T, Wi, Li, c2, status, s))
             return rc;
     } else {
         // a cluster splits the query tiles while the CTAs do not fill the SMs twice

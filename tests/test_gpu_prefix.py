@@ -97,3 +97,19 @@ def test_scores_that_rise_beyond_every_power_of_two(B, Hkv, G, D, S, P):
         swa.device_status()
         tol = ref.decode_tol(want, spread, 0.0, 128, 2.0 ** -8)
         assert bool(((out.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("B,Hkv,G,P", [(100, 2, 3, 1500), (24, 2, 4, 1100), (2, 2, 2, 100), (2, 1, 12, 300)])
+def test_a_scale_below_fp32(B, Hkv, G, P):
+    """A scale that fp32 holds only as 0 gives equal weights: the keys past a ragged end stay out."""
+    D, S = 128, 9
+    g = gen(P + 1)
+    q, kp, vp = rand(g, B, Hkv * G, D), rand(g, Hkv, P, D), rand(g, Hkv, P, D)
+    kc, vc = rand(g, B, Hkv, S, D), rand(g, B, Hkv, S, D)
+    vs = torch.cat([vp.expand(B, Hkv, P, D), vc], 2).double()
+    want = vs.mean(2).repeat_interleave(G, 1)
+    tol = ref.decode_tol(want, vs.abs().mean(2).repeat_interleave(G, 1), 0.0, P + S, ref.UBF)
+    for scale in (1e-38, 1e-46, 1e-300):
+        out = swa.prefix_decode(q, kp, vp, kc, vc, torch.full((B,), S, device=DEV), S, scale=scale)
+        assert bool(((out.double() - want).abs() <= tol).all()), scale
+    swa.device_status()
