@@ -378,7 +378,7 @@ int swa_decode_noalloc(const void* q, const void* kring, const void* vring, cons
  *
  * with n = lens[b] (T when lens is NULL) tokens in stream b, of which the last `last` are
  * counted as queries: max(0, n - last) <= i < n. Keys j >= n, and keys that no counted query
- * sees, get 0. Rows of q, k and lse at or past n are not used.
+ * sees (all of them for H = 0), get 0. Rows of q, k and lse at or past n are not used.
  *   q       : [B,H,T,D], k: [B,Hkv,T,D] of `dtype`; strides NULL (contiguous) or 6 element
  *             strides q(b,h,t), k(b,h,t) as in swa_forward_ex.
  *   lse     : [B,H,T] fp32 contiguous, as swa_forward_lse writes it for the same scale and W.

@@ -469,8 +469,9 @@ int swa_key_weights(const void* q, const void* k, const float* lse, const int64_
     if (last < 1) return fail(SWA_ERR_INVALID_ARG, "%s: last=%lld must be >= 1", fn, (long long)last);
     float c2;
     if (int rc = scale_log2(fn, scale, &c2)) return rc;
-    if (B == 0 || H == 0 || T == 0) return success();
-    if (!q || !k || !lse || !weights) return fail(SWA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (B == 0 || Hkv == 0 || T == 0) return success();
+    if (!weights || (H > 0 && (!q || !k || !lse))) return fail(SWA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (Hkv > INT32_MAX || B > INT32_MAX / Hkv) return fail(SWA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     if (dtype == SWA_BF16) {
         if (int rc = check_head_dim(fn, D)) return rc;
     } else if (D > 4096) {
@@ -495,7 +496,7 @@ int swa_key_weights(const void* q, const void* k, const float* lse, const int64_
     int *status, num_sms;
     if (int rc = swa_internal::device_info(&status, &num_sms)) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == SWA_BF16) {
+    if (dtype == SWA_BF16 && H > 0) {
         CUtensorMap tm_q, tm_k;
         if (int rc = swa_internal::tensor_map(&tm_q, q, B, H, T, D, qs, swa::kKwSlice)) return rc;
         if (int rc = swa_internal::tensor_map(&tm_k, k, B, Hkv, T, D, ks, 128)) return rc;
@@ -503,6 +504,7 @@ int swa_key_weights(const void* q, const void* k, const float* lse, const int64_
                               : launch_key_weights<64>(tm_q, tm_k, lse, lens, weights, B, H, Hkv, T, Wi, Li, c2, status, s))
             return rc;
     } else {
+        // (also for no query heads of either type: every sum is 0 and q, k, lse are not read)
         // a cluster splits the query tiles while the CTAs do not fill the SMs twice
         const int64_t units = B * Hkv * n_kt, tiles = H / Hkv * ((swa::kKwTile + (Wi < Li ? Wi : Li) + 62) / swa::kKwTile);
         int C = 1;
