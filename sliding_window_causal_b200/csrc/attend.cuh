@@ -177,7 +177,8 @@ struct AttendState {
 template <int D>
 struct AttendJoin {
     float m[kAttendWarps][kAttendQueries], l[kAttendWarps][kAttendQueries];
-    float o[kAttendWarps][kAttendQueries][D + 8];
+    alignas(16) float o[kAttendWarps][kAttendQueries][D + 8];  // read and written 16 bytes at a time
+    static_assert((D + 8) * sizeof(float) % 16 == 0, "a row of o starts on 16 bytes");
 
     template <typename Done>
     __device__ __forceinline__ void run(AttendState<D>& st, int nq, int tid, Done done) {
@@ -224,6 +225,8 @@ struct AttendJoin {
         }
     }
 };
+
+static_assert(alignof(AttendJoin<64>) >= 16 && alignof(AttendJoin<128>) >= 16, "16-byte accesses of o");
 
 // ------------------------------------------------------------------ splits of any number
 // CTA = (stream, key head, 8 of its queries, split of the slots 0 .. min(pos+1, S)-1).
