@@ -13,12 +13,12 @@ from test_gpu_serving import BF, DEV, gen, heavy, rand
 pytestmark = pytest.mark.gpu
 
 
-def exact_rows(q, kc, vc, pos, kp, vp):
+def exact_rows(q, kc, vc, pos, kp, vp, c=None):
     """(out, centred, spread, gain, ez) in float64: out, the sums of p |v - out| and of p |v|, the
     weight that each slot gets, and how far fp32 scores may move an exponent."""
     B, H, D = q.shape
     Hkv, S = kc.shape[1], kc.shape[2]
-    G, c = H // Hkv, 1 / math.sqrt(D)
+    G, c = H // Hkv, 1 / math.sqrt(D) if c is None else c
     out, centred, spread = (torch.zeros(B, H, D, dtype=torch.float64, device=DEV) for _ in range(3))
     gain = torch.zeros(B, Hkv, S, dtype=torch.float64, device=DEV)
     ez = 0.0
@@ -38,22 +38,27 @@ def exact_rows(q, kc, vc, pos, kp, vp):
     return out, centred, spread, gain, ez
 
 
+def pair_tol(want, centred, spread, ez, adds):
+    """Bound where weights may be one bf16 part. A weight rounded to bf16 is off by at most 2^-8 of
+    itself, in the product and in the sum that the output is divided by, so of a split's output o
+    it moves sum p e (v - o), at most 2^-8 sum p |v - o| over the split (1 + 2^-7 for the
+    divisor). The distance to the split's own mean is at most twice that to any other point, here
+    the whole row's output. The rest: exponents, hi + lo parts, sums in fp32."""
+    fine = 2 * ez + 2.0 ** -20 + 2.0 ** -15 + 2 * adds * ref.U32
+    return ref.UBF * want.abs() + (1 + ref.UBF) * (2 * ref.UBF * (1 + 2.0 ** -7) * centred + fine * spread)
+
+
 @pytest.mark.parametrize("B,Hkv,G,D,S,P,scale", [
     (100, 2, 3, 64, 33, 1500, 4), (40, 2, 4, 128, 20, 4000, 8), (48, 1, 4, 128, 9, 9000, 8), (200, 2, 2, 64, 1, 3000, 8),
     (129, 1, 1, 128, 5, 3300, 16)])
 def test_rows_that_few_keys_dominate(B, Hkv, G, D, S, P, scale):
-    """Queries scaled up, so that one or a few keys hold most of a row's weight. A weight rounded
-    to bf16 is off by at most 2^-8 of itself, in the product and in the sum that the output is
-    divided by, so of a split's output o it moves sum p e (v - o), at most 2^-8 sum p |v - o|
-    over the split (1 + 2^-7 for the divisor). The distance to the split's own mean is at most
-    twice that to any other point, here the whole row's output."""
+    """Queries scaled up, so that one or a few keys hold most of a row's weight."""
     g = gen(B + P + scale)
     q = rand(g, B, Hkv * G, D, scale=float(scale))
     kc, vc, kp, vp = rand(g, B, Hkv, S, D), rand(g, B, Hkv, S, D), rand(g, Hkv, P, D), rand(g, Hkv, P, D)
     pos = torch.randint(0, 2 * S, (B,), generator=g, device=DEV)
     want, centred, spread, gain, ez = exact_rows(q, kc, vc, pos, kp, vp)
-    fine = 2 * ez + 2.0 ** -20 + 2.0 ** -15 + 2 * (P + S) * ref.U32  # exponents, hi + lo parts, sums in fp32
-    tol = ref.UBF * want.abs() + (1 + ref.UBF) * (2 * ref.UBF * (1 + 2.0 ** -7) * centred + fine * spread)
+    tol = pair_tol(want, centred, spread, ez, P + S)
     before = heavy(g, B, Hkv, S)
     after = before.clone()
     for out in (swa.prefix_decode(q, kp, vp, kc, vc, pos, S), swa.cache_decode(q, kc, vc, after, pos, kp, vp)):
@@ -112,4 +117,93 @@ def test_a_scale_below_fp32(B, Hkv, G, P):
     for scale in (1e-38, 1e-46, 1e-300):
         out = swa.prefix_decode(q, kp, vp, kc, vc, torch.full((B,), S, device=DEV), S, scale=scale)
         assert bool(((out.double() - want).abs() <= tol).all()), scale
+    swa.device_status()
+
+
+def few_units(g, heads, n, D):
+    """[heads, n, D] of -1, 0 and 1 in random order, whose columns sum to at most 100 in magnitude."""
+    half = max(0, (n - 100) // 2)
+    a = torch.randint(-1, 2, (heads, half, D), generator=g, device=DEV)
+    v = torch.cat([a, -a, torch.randint(-1, 2, (heads, n - 2 * half, D), generator=g, device=DEV)], 1)
+    return v[:, torch.randperm(n, generator=g, device=DEV)]
+
+
+# B, Hkv, G, D, P; key tiles that a CTA takes, and what follows the prefix's kernel
+MANY_TILES = [
+    (40, 8, 4, 128, 33000),   # two row tiles, 15, then the streams
+    (40, 8, 4, 64, 33001),    # 15
+    (128, 8, 4, 128, 65536),  # 57
+    (200, 4, 2, 64, 50003),   # 22
+    (70, 1, 7, 128, 60011),   # 8, the streams beside it
+    (33, 3, 12, 128, 20000),  # 7, then the splits of more than 8 heads
+    (64, 8, 1, 64, 70001),    # one row tile on two lanes, 31, then the streams
+    (64, 32, 1, 128, 8192),   # 16
+    (2, 1, 1, 128, 140000),   # 9, the streams beside it
+    (3, 2, 12, 64, 150001),   # then splits
+]
+
+
+@pytest.mark.parametrize("B,Hkv,G,D,P", MANY_TILES)
+def test_every_key_of_a_long_prefix_counts_once(B, Hkv, G, D, P):
+    """Queries of zeros give every key the same weight, 1, and values of -1, 0 and 1 make every sum
+    a whole number of at most 120: one key lost, doubled or out of place changes its columns by
+    1 in 120 or more, twice the step of bf16. Nothing but the output is rounded."""
+    S = 20
+    g = gen(P + B)
+    q = torch.zeros(B, Hkv * G, D, dtype=BF, device=DEV)
+    kp, kc = rand(g, Hkv, P, D), rand(g, B, Hkv, S, D)
+    pv, sv = few_units(g, Hkv, P, D), torch.randint(-1, 2, (B, Hkv, S, D), generator=g, device=DEV)
+    pos = torch.randint(0, 2 * S, (B,), generator=g, device=DEV)
+    n = (pos + 1).clamp_max(S)
+    seen = torch.arange(S, device=DEV) < n[:, None]
+    total = pv.sum(1) + (sv * seen[:, None, :, None]).sum(2)
+    assert int(total.abs().max()) <= 120
+    want = (total.double() / (P + n)[:, None, None]).repeat_interleave(G, 1)
+    wc = torch.zeros(B, Hkv, S, device=DEV)
+    vp, vc = pv.to(BF), sv.to(BF)
+    for out in (swa.prefix_decode(q, kp, vp, kc, vc, pos, S), swa.cache_decode(q, kc, vc, wc, pos, kp, vp)):
+        off = (out.double() - want).abs()
+        assert bool((off <= want.abs() * (ref.UBF + 2.0 ** -16)).all()), int((off > want.abs() * 0.004).sum())
+    gain = torch.where(seen, G / (P + n).double()[:, None], 0.0)[:, None].expand(B, Hkv, S)
+    assert bool(((wc.double() - gain).abs() <= gain * 2.0 ** -18).all())  # log2 and exp2 of 18 bits and less
+    swa.device_status()
+
+
+@pytest.mark.parametrize("scale", [None, 1.0])
+@pytest.mark.parametrize("B,Hkv,G,D,P", MANY_TILES)
+def test_scores_that_grow_along_a_long_prefix(B, Hkv, G, D, P, scale):
+    """Scores that rise by 0.3 to 10 (powers of two) a key tile, so that a CTA moves its reference in
+    tiles after its first ones: a few streams in float64, the others by repeating the call."""
+    S = 30
+    g = gen(P + D)
+    q = rand(g, B, Hkv * G, D).abs() + 1
+    ramp = torch.linspace(-3, 3, P, device=DEV)[:, None]
+    kp = (rand(g, Hkv, P, D).float() * 0.1 + ramp).to(BF)
+    kc, vp, vc = rand(g, B, Hkv, S, D), rand(g, Hkv, P, D), rand(g, B, Hkv, S, D)
+    pos = torch.randint(0, 2 * S, (B,), generator=g, device=DEV)
+    for _ in range(2):
+        out = swa.prefix_decode(q, kp, vp, kc, vc, pos, S, scale=scale)
+        assert torch.equal(out, swa.prefix_decode(q, kp, vp, kc, vc, pos, S, scale=scale))
+        some = [0, B // 2, B - 1]
+        c = 1 / math.sqrt(D) if scale is None else scale
+        want, centred, spread, _, ez = exact_rows(q[some], kc[some], vc[some], pos[some], kp, vp, c)
+        off = (out[some].double() - want).abs()
+        tol = pair_tol(want, centred, spread, ez, 2000)  # additions in a row: 16 products a tile, 57 tiles, and joins
+        assert bool((off <= tol).all()), float((off / tol).max())
+        kp, vp = kp.flip(1).contiguous(), vp.flip(1).contiguous()
+    swa.device_status()
+
+
+@pytest.mark.parametrize("B,Hkv,G,D,S,P", [(130, 1, 1, 128, 3, 257), (32, 2, 8, 64, 31, 640), (100, 2, 3, 64, 33, 700)])
+def test_a_short_prefix_of_many_rows_keeps_two_parts(B, Hkv, G, D, S, P):
+    """More than 128 rows share these prefixes, yet each stream reads them by itself (no workspace),
+    with its weights as hi + lo parts: the bound of 2^-16 of a weight holds."""
+    assert swa.prefix_decode_workspace_bytes(B, Hkv * G, Hkv, S, P, D) == 0
+    g = gen(B + P)
+    q, kp, vp = rand(g, B, Hkv * G, D), rand(g, Hkv, P, D), rand(g, Hkv, P, D)
+    kc, vc = rand(g, B, Hkv, S, D), rand(g, B, Hkv, S, D)
+    pos = torch.randint(0, 2 * S, (B,), generator=g, device=DEV)
+    want, spread, _, ez = ref.decode(q, kc, vc, pos, kp, vp)
+    off = (swa.prefix_decode(q, kp, vp, kc, vc, pos, S).double() - want).abs()
+    assert bool((off <= ref.decode_tol(want, spread, ez, P + S, 2.0 ** -16)).all())
     swa.device_status()
