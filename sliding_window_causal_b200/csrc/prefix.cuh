@@ -23,13 +23,14 @@
 // 0.125 and 0.122 ms. 64 streams of 32 heads (!PAIR): 72 us more for 24576 more keys, 5.6 TB/s.
 //
 // P is rounded to bf16. !PAIR carries it as hi + lo parts (2^-16), for the second product costs
-// nothing there. PAIR is bound by tensor core and exponentials: a warp carries two parts only of a
-// tile in which a key of one of its rows weighs more than a third of what the row has met before
-// (so it could end up above a quarter), and one part of the others, each weight off by up to 2^-8
-// of itself. So that the error of a key that weighs much cancels, o is divided by the sum of the
-// weights as the products took them: it is scaled by l / l', with l' that sum, and (m, l) stay
-// those of the fp32 weights, from which the slots' own weights grow. What is left is at most 2^-8
-// sum p |v - o| over the keys of one part.
+// nothing there. PAIR is bound by tensor core and exponentials: a row carries two parts only of a
+// tile in which one of its keys weighs more than a third of what it has met before (so it could
+// end up above a quarter; a warp none of whose rows does skips the second product), and one part
+// of the others, each weight off by up to 2^-8 of itself. Each row chooses by its own scores, so
+// no stream's output depends on another's. So that the error of a key that weighs much cancels, o
+// is divided by the sum of the weights as the products took them: it is scaled by l / l', with l'
+// that sum, and (m, l) stay those of the fp32 weights, from which the slots' own weights grow.
+// What is left is at most 2^-8 sum p |v - o| over the keys of one part.
 #pragma once
 #include <cuda_bf16.h>
 #include <math.h>
@@ -65,15 +66,15 @@ struct PrefixCfg {
 
 // P = 2^(s c - mu) of the thread's 128 scores v (c = scale_log2), over S at TMEM column scol as bf16
 // pairs: keys 32k .. 32k+31 in columns 32k .. 32k+15 and, with LO, the rest p - bf16(p), again
-// bf16, in columns 32k+16 .. 32k+31. after_part(p): part p of P is stored, with one more chunk's
-// arithmetic behind it. l grows by the fp32 weights, lw by the weights as written (with LO they
-// are the same to 2^-17).
-template <bool LO, typename AfterPart>
-__device__ __forceinline__ void prefix_exps(uint32_t scol, const uint32_t (&v)[4][32], float scale_log2, float mu, float& l,
-                                            float& lw, AfterPart after_part) {
+// bf16, in columns 32k+16 .. 32k+31 (LO = 2: of this row only if lo is set, else zeros).
+// after_part(p): part p of P is stored, with one more chunk's arithmetic behind it. l grows by the
+// fp32 weights, lw by the weights as written (with the rest they are the same to 2^-17).
+template <int LO, typename AfterPart>
+__device__ __forceinline__ void prefix_exps(uint32_t scol, const uint32_t (&v)[4][32], float scale_log2, float mu, bool lo,
+                                            float& l, float& lw, AfterPart after_part) {
     const ptx::f32x2 sc = {scale_log2, scale_log2}, nm = {-mu, -mu};
-    ptx::f32x2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-    ptx::f32x2 accw[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+    ptx::f32x2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+    ptx::f32x2 accw[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         uint32_t ph[16], pl[16];
@@ -81,31 +82,31 @@ __device__ __forceinline__ void prefix_exps(uint32_t scol, const uint32_t (&v)[4
         for (int t = 0; t < 16; ++t) {
             const ptx::f32x2 z = ptx::fma2({__uint_as_float(v[c][2 * t]), __uint_as_float(v[c][2 * t + 1])}, sc, nm);
             const ptx::f32x2 e = {ptx::ex2(z.x), ptx::ex2(z.y)};
-            acc[t & 3] = ptx::add2(acc[t & 3], e);
+            acc[t % 2] = ptx::add2(acc[t % 2], e);
             ph[t] = ptx::pack_bf16x2(e.x, e.y);
-            if (LO) {
+            if (LO != 0) {
                 const ptx::f32x2 r = ptx::sub2(e, {ptx::bf16lo_f32(ph[t]), ptx::bf16hi_f32(ph[t])});
-                pl[t] = ptx::pack_bf16x2(r.x, r.y);
-            } else {
-                accw[t & 3] = ptx::add_bf16x2_f32(ph[t], accw[t & 3]);
+                pl[t] = LO == 2 && !lo ? 0u : ptx::pack_bf16x2(r.x, r.y);
             }
+            if (LO != 1) accw[t % 2] = ptx::add_bf16x2_f32(ph[t], accw[t % 2]);
         }
         if (c > 0 && c % (4 / kPPParts) == 0) after_part(c / (4 / kPPParts) - 1);
         ptx::tmem_st16(scol + 32 * c, ph);
-        if (LO) ptx::tmem_st16(scol + 32 * c + 16, pl);
+        if (LO != 0) ptx::tmem_st16(scol + 32 * c + 16, pl);
     }
     after_part(kPPParts - 1);
-    const float e = ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) + ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y));
+    const float e = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
     l += e;
-    if (LO) lw += e;
-    else lw += ((accw[0].x + accw[0].y) + (accw[1].x + accw[1].y)) + ((accw[2].x + accw[2].y) + (accw[3].x + accw[3].y));
+    if (LO == 1 || (LO == 2 && lo)) lw += e;
+    else lw += (accw[0].x + accw[0].y) + (accw[1].x + accw[1].y);
 }
 
 // One tile of one row: the thread's 128 scores at TMEM column scol become P in place, relative to
 // m, the row's reference (-inf before its first tile): a row whose maximum passes it by more than
 // 2^8 moves it up by a whole power of two, which rescales O (at ocol), l and lw exactly. TAIL:
-// only columns 0 .. last are keys. ADAPT: the warp chooses whether P has low parts, and
-// publish(bool) says so before the first part is handed over; else it always has.
+// only columns 0 .. last are keys. ADAPT: the row chooses whether P has low parts, and
+// publish(bool) says before the first part is handed over whether any row of the warp did; else it
+// always has.
 template <int D, bool TAIL, bool ADAPT, typename AfterPart, typename Publish>
 __device__ __forceinline__ void prefix_tile(uint32_t scol, uint32_t ocol, float scale_log2, float& m, float& l, float& lw,
                                             int last, AfterPart after_part, Publish publish) {
@@ -149,12 +150,13 @@ __device__ __forceinline__ void prefix_tile(uint32_t scol, uint32_t ocol, float 
     if (m == -INFINITY) m = tm;
     const float mu = m == -INFINITY ? 0.f : m;
     if constexpr (ADAPT) {
-        const bool lo = __any_sync(0xffffffffu, tm != -INFINITY && 3.f * ptx::ex2(tm - mu) > l);
-        publish(lo);
-        if (lo) prefix_exps<true>(scol, v, scale_log2, mu, l, lw, after_part);
-        else prefix_exps<false>(scol, v, scale_log2, mu, l, lw, after_part);
+        const bool lo = tm != -INFINITY && 3.f * ptx::ex2(tm - mu) > l;
+        const bool any = __any_sync(0xffffffffu, lo);
+        publish(any);
+        if (any) prefix_exps<2>(scol, v, scale_log2, mu, lo, l, lw, after_part);
+        else prefix_exps<0>(scol, v, scale_log2, mu, lo, l, lw, after_part);
     } else {
-        prefix_exps<true>(scol, v, scale_log2, mu, l, lw, after_part);
+        prefix_exps<1>(scol, v, scale_log2, mu, true, l, lw, after_part);
     }
 }
 

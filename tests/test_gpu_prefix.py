@@ -207,3 +207,19 @@ def test_a_short_prefix_of_many_rows_keeps_two_parts(B, Hkv, G, D, S, P):
     off = (swa.prefix_decode(q, kp, vp, kc, vc, pos, S).double() - want).abs()
     assert bool((off <= ref.decode_tol(want, spread, ez, P + S, 2.0 ** -16)).all())
     swa.device_status()
+
+
+@pytest.mark.parametrize("D,P", [(64, 33001), (128, 30011)])
+def test_a_stream_does_not_depend_on_its_neighbours(D, P):
+    """Rows of 40 streams share tiles, and some of a stream's weights have low parts where its scores
+    are sharp: another stream's queries must not change a bit of this one's output."""
+    B, Hkv, G, S = 40, 2, 4, 10
+    g = gen(P)
+    q, kp, vp = rand(g, B, Hkv * G, D), rand(g, Hkv, P, D), rand(g, Hkv, P, D)
+    kc, vc = rand(g, B, Hkv, S, D), rand(g, B, Hkv, S, D)
+    pos = torch.full((B,), 2 * S, device=DEV)
+    a = swa.prefix_decode(q, kp, vp, kc, vc, pos, S)
+    q[::2] *= 8
+    b = swa.prefix_decode(q, kp, vp, kc, vc, pos, S)
+    assert torch.equal(a[1::2], b[1::2]) and not torch.equal(a[::2], b[::2])
+    swa.device_status()
