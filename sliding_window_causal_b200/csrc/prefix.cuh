@@ -19,18 +19,16 @@
 // in the layout of a TMA tile, since G query heads of 128 / G streams are no box for every G.
 //
 // Measured, D = 128: 128 streams of 32 heads, 4 to a key head, behind 65536 keys (PAIR, 137 GFLOP):
-// 0.118 ms, 1.16 PFLOP/s; hi + lo parts there 0.148 ms, P handed over in 1 or 4 parts instead of 2
-// 0.125 and 0.122 ms. 64 streams of 32 heads (!PAIR): 72 us more for 24576 more keys, 5.6 TB/s.
+// 0.152 ms (0.165 where few keys dominate the rows), 0.9 PFLOP/s of the formula, 1.36 of the products
+// issued. 64 streams of 32 heads (!PAIR): 67 us more for 24576 more keys, 6.0 TB/s.
 //
-// P is rounded to bf16. !PAIR carries it as hi + lo parts (2^-16), for the second product costs
-// nothing there. PAIR is bound by tensor core and exponentials: a row carries two parts only of a
-// tile in which one of its keys weighs more than a third of what it has met before (so it could
-// end up above a quarter; a warp none of whose rows does skips the second product), and one part
-// of the others, each weight off by up to 2^-8 of itself. Each row chooses by its own scores, so
-// no stream's output depends on another's. So that the error of a key that weighs much cancels, o
-// is divided by the sum of the weights as the products took them: it is scaled by l / l', with l'
-// that sum, and (m, l) stay those of the fp32 weights, from which the slots' own weights grow.
-// What is left is at most 2^-8 sum p |v - o| over the keys of one part.
+// P is carried as hi + lo bf16 parts (2^-16 of a weight), so that the output is rounded once, as in
+// the streams' kernels, and a stream's precision does not depend on how many rows share the prefix.
+// !PAIR has room for the second product; PAIR is bound by the products. Of one part only, there
+// 0.125 ms, a key that holds much of a row's weight is off by up to 2^-8 of itself: queries scaled
+// by 8 gave 0.019 on outputs below 4 (0.011 if divided by the sum of the rounded weights) where two
+// parts give 0.0078, the output's own rounding. Two parts only in the tiles of such keys: 0.133 ms
+// for even rows, but 0.225 for those.
 #pragma once
 #include <cuda_bf16.h>
 #include <math.h>
@@ -57,59 +55,21 @@ struct PrefixCfg {
     // q_full, ring_full[S], ring_empty[S], s_full[2], p_full[2][kPPParts], o_final[2], drain
     static constexpr int kNumBars = 1 + 2 * kStages + 2 + 2 * kPPParts + 2 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-    static constexpr int kLoOff = (kMiscOff + 8 + 15) & ~15;  // low-part flags [2 lanes][2 parities][4 warps]
-    static constexpr int kSmemBytes = kLoOff + 64 + 1024;
+    static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
     static constexpr uint32_t kTmemCols = 512;
     __device__ static constexpr uint32_t colS(int x) { return 128u * x; }
     __device__ static constexpr uint32_t colO(int x) { return 256u + 128u * x; }
 };
 
-// P = 2^(s c - mu) of the thread's 128 scores v (c = scale_log2), over S at TMEM column scol as bf16
-// pairs: keys 32k .. 32k+31 in columns 32k .. 32k+15 and, with LO, the rest p - bf16(p), again
-// bf16, in columns 32k+16 .. 32k+31 (LO = 2: of this row only if lo is set, else zeros).
-// after_part(p): part p of P is stored, with one more chunk's arithmetic behind it. l grows by the
-// fp32 weights, lw by the weights as written (with the rest they are the same to 2^-17).
-template <int LO, typename AfterPart>
-__device__ __forceinline__ void prefix_exps(uint32_t scol, const uint32_t (&v)[4][32], float scale_log2, float mu, bool lo,
-                                            float& l, float& lw, AfterPart after_part) {
-    const ptx::f32x2 sc = {scale_log2, scale_log2}, nm = {-mu, -mu};
-    ptx::f32x2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
-    ptx::f32x2 accw[2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t ph[16], pl[16];
-#pragma unroll
-        for (int t = 0; t < 16; ++t) {
-            const ptx::f32x2 z = ptx::fma2({__uint_as_float(v[c][2 * t]), __uint_as_float(v[c][2 * t + 1])}, sc, nm);
-            const ptx::f32x2 e = {ptx::ex2(z.x), ptx::ex2(z.y)};
-            acc[t % 2] = ptx::add2(acc[t % 2], e);
-            ph[t] = ptx::pack_bf16x2(e.x, e.y);
-            if (LO != 0) {
-                const ptx::f32x2 r = ptx::sub2(e, {ptx::bf16lo_f32(ph[t]), ptx::bf16hi_f32(ph[t])});
-                pl[t] = LO == 2 && !lo ? 0u : ptx::pack_bf16x2(r.x, r.y);
-            }
-            if (LO != 1) accw[t % 2] = ptx::add_bf16x2_f32(ph[t], accw[t % 2]);
-        }
-        if (c > 0 && c % (4 / kPPParts) == 0) after_part(c / (4 / kPPParts) - 1);
-        ptx::tmem_st16(scol + 32 * c, ph);
-        if (LO != 0) ptx::tmem_st16(scol + 32 * c + 16, pl);
-    }
-    after_part(kPPParts - 1);
-    const float e = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-    l += e;
-    if (LO == 1 || (LO == 2 && lo)) lw += e;
-    else lw += (accw[0].x + accw[0].y) + (accw[1].x + accw[1].y);
-}
-
-// One tile of one row: the thread's 128 scores at TMEM column scol become P in place, relative to
-// m, the row's reference (-inf before its first tile): a row whose maximum passes it by more than
-// 2^8 moves it up by a whole power of two, which rescales O (at ocol), l and lw exactly. TAIL:
-// only columns 0 .. last are keys. ADAPT: the row chooses whether P has low parts, and
-// publish(bool) says before the first part is handed over whether any row of the warp did; else it
-// always has.
-template <int D, bool TAIL, bool ADAPT, typename AfterPart, typename Publish>
-__device__ __forceinline__ void prefix_tile(uint32_t scol, uint32_t ocol, float scale_log2, float& m, float& l, float& lw,
-                                            int last, AfterPart after_part, Publish publish) {
+// One tile of one row: the thread's 128 scores at TMEM column scol become P = 2^(z - m), z = s c
+// (c = scale_log2), in place as bf16 pairs: keys 32k .. 32k+31 in columns 32k .. 32k+15 and the
+// rest p - bf16(p), again bf16, in columns 32k+16 .. 32k+31. TAIL: only columns 0 .. last are
+// keys. m is the row's reference (-inf before its first tile): a row whose maximum passes it by
+// more than 2^8 moves it up by a whole power of two, which rescales O (at ocol) and l exactly.
+// after_part(p): part p of P is stored, with one more chunk's arithmetic behind it.
+template <int D, bool TAIL, typename AfterPart>
+__device__ __forceinline__ void prefix_tile(uint32_t scol, uint32_t ocol, float scale_log2, float& m, float& l, int last,
+                                            AfterPart after_part) {
     uint32_t v[4][32];
 #pragma unroll
     for (int c = 0; c < 4; ++c) ptx::tmem_ld32(scol + 32 * c, v[c]);
@@ -144,20 +104,30 @@ __device__ __forceinline__ void prefix_tile(uint32_t scol, uint32_t ocol, float 
         __syncwarp();
         pp_rescale<D, false>(ocol, scol, 0, f);
         l *= f;
-        lw *= f;
         m = gone ? tm : m + up;
     }
     if (m == -INFINITY) m = tm;
     const float mu = m == -INFINITY ? 0.f : m;
-    if constexpr (ADAPT) {
-        const bool lo = tm != -INFINITY && 3.f * ptx::ex2(tm - mu) > l;
-        const bool any = __any_sync(0xffffffffu, lo);
-        publish(any);
-        if (any) prefix_exps<2>(scol, v, scale_log2, mu, lo, l, lw, after_part);
-        else prefix_exps<0>(scol, v, scale_log2, mu, lo, l, lw, after_part);
-    } else {
-        prefix_exps<1>(scol, v, scale_log2, mu, true, l, lw, after_part);
+    const ptx::f32x2 sc = {scale_log2, scale_log2}, nm = {-mu, -mu};
+    ptx::f32x2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t ph[16], pl[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            const ptx::f32x2 z = ptx::fma2({__uint_as_float(v[c][2 * t]), __uint_as_float(v[c][2 * t + 1])}, sc, nm);
+            const ptx::f32x2 e = {ptx::ex2(z.x), ptx::ex2(z.y)};
+            acc[t & 1] = ptx::add2(acc[t & 1], e);
+            ph[t] = ptx::pack_bf16x2(e.x, e.y);
+            const ptx::f32x2 r = ptx::sub2(e, {ptx::bf16lo_f32(ph[t]), ptx::bf16hi_f32(ph[t])});
+            pl[t] = ptx::pack_bf16x2(r.x, r.y);
+        }
+        if (c > 0 && c % (4 / kPPParts) == 0) after_part(c / (4 / kPPParts) - 1);
+        ptx::tmem_st16(scol + 32 * c, ph);
+        ptx::tmem_st16(scol + 32 * c + 16, pl);
     }
+    after_part(kPPParts - 1);
+    l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
 }
 
 // a: q, ml, o, B, H, Hkv, G, S (prefix length), chunk (key tiles a split takes), NS, scale_log2
@@ -179,8 +149,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     uint64_t* drain = o_final + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cf::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cf::kMiscOff + 4);
-    // [4 (2x + parity) + w]: warp w of lane x wrote low parts of P for the tile of that parity
-    volatile uint32_t* lo_flag = reinterpret_cast<volatile uint32_t*>(smem + Cf::kLoOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     const int n_rows = a.B * a.G;
@@ -281,31 +249,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             };
             auto issue_pv = [&](int x, uint32_t L, int j) {  // O_x (+)= P_x V as the parts of P arrive
                 const uint32_t v_lo = (ring_lo + L % NS * kTileLo) | lo_v;
-                bool some = true;  // some warp of the lane wrote low parts; dis: the rows of those that did not
-                uint32_t dis[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
                 for (int part = 0; part < kPPParts; ++part) {
                     if (ok) ok = pp_wait_warp(p_full + kPPParts * x + part, j & 1, wait_limit_ns, abort_flag);
                     if (!ok) return;
                     ptx::tc_fence_after();
                     constexpr int kPer = 8 / kPPParts;
-                    const uint32_t p_col = tmem + Cf::colS(x), o_col = tmem + Cf::colO(x);
 #pragma unroll
-                    for (int kk = part * kPer; kk < (part + 1) * kPer; ++kk)
-                        ptx::mma_ts_one(o_col, p_col + pp_pcol(kk), desc_hi | (v_lo + kk * (2048 >> 4)), idesc_o,
-                                        (j > 0 || kk > 0) ? 1u : 0u);
-                    if (PAIR && part == 0) some = pp_lo_lanes(lo_flag, x, j, dis);
-                    if (PAIR && some && (dis[0] | dis[1] | dis[2] | dis[3]) != 0u) {
+                    for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                         for (int kk = part * kPer; kk < (part + 1) * kPer; ++kk)
-                            ptx::mma_ts_one_masked(o_col, p_col + pp_pcol(kk) + 16, desc_hi | (v_lo + kk * (2048 >> 4)),
-                                                   idesc_o, 1u, dis);
-                    } else if (some) {
-#pragma unroll
-                        for (int kk = part * kPer; kk < (part + 1) * kPer; ++kk)
-                            ptx::mma_ts_one(o_col, p_col + pp_pcol(kk) + 16, desc_hi | (v_lo + kk * (2048 >> 4)),
-                                            idesc_o, 1u);
-                    }
+                            ptx::mma_ts_one(tmem + Cf::colO(x), tmem + Cf::colS(x) + pp_pcol(kk) + 16 * lo,
+                                            desc_hi | (v_lo + kk * (2048 >> 4)), idesc_o,
+                                            (j > 0 || kk > 0 || lo > 0) ? 1u : 0u);
                 }
             };
             if (PAIR) {
@@ -382,7 +338,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t scol = tl + Cf::colS(x), ocol = tl + Cf::colO(x);
         const int mine = PAIR ? n : (n + 1 - x) / 2;
-        float m = -INFINITY, l = 0.f, lw = 0.f;
+        float m = -INFINITY, l = 0.f;
         bool ok = true;
         // S_x(j) follows P_x(j-1) V in the tensor core's order: once S_x(j) is there, O_x is at rest
         auto after_part = [&](int part) {
@@ -392,22 +348,18 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             if (lane == 0) ptx::mbar_arrive(p_full + kPPParts * x + part);
         };
         for (int j = 0; j < mine; ++j) {
-            auto publish = [&](bool lo) {
-                if (lane == 0) lo_flag[4 * (2 * x + (j & 1)) + quarter] = lo ? 1u : 0u;
-            };
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full + x, j & 1, wait_limit_ns, abort_flag));
             if (!ok) break;
             ptx::tc_fence_after();
             const int last = a.S - 1 - 128 * (t0 + (PAIR ? j : 2 * j + x));  // last key of the tile
-            if (last >= 127) prefix_tile<D, false, PAIR>(scol, ocol, a.scale_log2, m, l, lw, 127, after_part, publish);
-            else prefix_tile<D, true, PAIR>(scol, ocol, a.scale_log2, m, l, lw, last, after_part, publish);
+            if (last >= 127) prefix_tile<D, false>(scol, ocol, a.scale_log2, m, l, 127, after_part);
+            else prefix_tile<D, true>(scol, ocol, a.scale_log2, m, l, last, after_part);
         }
         const int64_t at = qrow * a.NS + (int)blockIdx.y;
         if (PAIR) {
             if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(o_final + x, 0, wait_limit_ns, abort_flag));
             if (ok) {
                 ptx::tc_fence_after();
-                const float f = lw > 0.f ? l / lw : 1.f;  // neither is where every score is NaN or -inf
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -418,8 +370,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                         float4* to = reinterpret_cast<float4*>(a.o + at * D + 32 * c);
 #pragma unroll
                         for (int t = 0; t < 8; ++t)
-                            to[t] = make_float4(__uint_as_float(o[4 * t]) * f, __uint_as_float(o[4 * t + 1]) * f,
-                                                __uint_as_float(o[4 * t + 2]) * f, __uint_as_float(o[4 * t + 3]) * f);
+                            to[t] = make_float4(__uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]),
+                                                __uint_as_float(o[4 * t + 2]), __uint_as_float(o[4 * t + 3]));
                     }
                 }
             }
