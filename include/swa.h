@@ -367,7 +367,11 @@ int swa_decode_noalloc(const void* q, const void* kring, const void* vring, cons
  * Usual order: swa_forward_lse on the prompt, swa_key_weights, swa_cache_seed; then for each
  * token swa_cache_append and swa_cache_decode.
  * The calls allocate nothing and can be captured into a graph; the first call on a device of
- * each kind sets kernel attributes and is made before any capture.
+ * each kind sets kernel attributes and is made before any capture. With B, Hkv or T = 0 nothing
+ * is read, written or reported. What a call must not use (rows at or past a stream's length,
+ * slots without a token, rows past the prefix) may hold anything, NaN and infinities too. A NaN
+ * that a query sees makes its output NaN; an infinite value that it sees makes its column of
+ * the output infinite or NaN, as its weight is carried in two parts.
  */
 
 /*

@@ -229,7 +229,10 @@ struct AttendJoin {
 static_assert(alignof(AttendJoin<64>) >= 16 && alignof(AttendJoin<128>) >= 16, "16-byte accesses of o");
 
 // ------------------------------------------------------------------ splits of any number
-// CTA = (stream, key head, 8 of its queries, split of the slots 0 .. min(pos+1, S)-1).
+// CTA = (stream, key head, 8 of its queries, split of the slots 0 .. min(pos+1, S)-1). More than 8
+// query heads to a key head read its keys and values once for each 8, mostly from L2: 64 streams of
+// 64 heads, 16 to a key head, 4096 slots, D = 128, with weights (545 MB): 144 us and 40 in
+// finish_kernel, which reads the scores again; 9 to a key head of 72 (1.09 GB) 271 and 47.
 template <int D, bool SCORES>
 __global__ void __launch_bounds__(kAttendWarps * 32, D == 128 ? 4 : 6) attend_kernel(const AttendArgs a) {
     __shared__ AttendJoin<D> join;

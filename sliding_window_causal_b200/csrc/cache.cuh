@@ -23,9 +23,11 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 // ------------------------------------------------------------------ append
-// One CTA per (b, hk). Bound by the 12 bytes a slot (weight, position) that the choice reads;
-// the loads of kAppendUnroll slots a thread are in flight together (64 streams, 32 heads, 4096
-// slots, 103 MB: 20 us, 5.2 TB/s; with 1, 2 or 8 in flight 24.7, 22.9 and 43.5 us).
+// One CTA per (b, hk), which reads 12 bytes a slot (weight, position); the loads of kAppendUnroll
+// slots a thread are in flight together. 64 streams, 32 heads, 4096 slots, 103 MB: 24 us, 4.3 TB/s
+// (0.65 of a copy's rate) on caches that are not in L2: 2048 short CTAs in 2.3 waves, none of which
+// has a load in flight while it reduces. Replayed on one set of caches, partly in L2, 21 us (there
+// 1, 2 or 8 slots in flight took 24.7, 22.9 and 43.5 us against 20).
 constexpr int kAppendThreads = 256;
 constexpr int kAppendUnroll = 4;
 __global__ void __launch_bounds__(kAppendThreads, 6)
@@ -128,9 +130,9 @@ constexpr int kSeedThreads = 512;
 // counts the digits of its run of positions; the counts meet in distributed shared memory. The
 // copy, 4 D bytes read and written a slot, is the bound; the passes over 4 bytes a position come
 // before it, each with the latency of its barriers, which is why they are spread over a cluster.
-// 32 heads, 16384 positions into 2048 slots, D = 128, 70 MB: 21.6 us, about half of it the
-// selection (with 8 bits a pass 22.7; with C = 1, 2, 4, 8 before the passes could end early 64,
-// 45, 29, 26).
+// 32 heads, 16384 positions into 2048 slots, D = 128, 70 MB: 27.7 us on prompts that are not in L2.
+// Replayed on one prompt 23, about half of it the selection (there with 8 bits a pass 22.7 against
+// 21.6; with C = 1, 2, 4, 8 before the passes could end early 64, 45, 29, 26).
 __global__ void __launch_bounds__(kSeedThreads)
     cache_seed_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                       const float* __restrict__ weights, const int64_t* __restrict__ lens, uint4* __restrict__ kc,

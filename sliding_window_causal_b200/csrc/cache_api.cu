@@ -222,13 +222,15 @@ int prefix_chunk(int64_t groups, int tiles, int least, int64_t rows, int64_t sms
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
 // A prefix of at most this many bytes, taken once for each stream, is left to stream_kernel: the
-// streams read it from L2, which costs less than a launch of its own and a join. 8 key heads,
-// slots 200, D = 128, own and not: 16 streams P 300 (20 MB) 9.8 and 11.1 us, 32 streams (39 MB)
-// 12.8 and 11.6, 16 streams P 1000 (66 MB) 14.6 and 11.4. Above 128 rows a key head, where the
-// streams' query heads share what they read and prefix_kernel has twice the rows to start with, 109
-// streams of 5 key heads, P 206 (57 MB) 12.3 and 22.4. With at most 8 rows, where prefix_kernel's
-// tiles are nearly empty, 2 streams P 4000 (66 MB) 13.2 and 20.1, 8 streams P 4000 (131 MB) 21.2
-// and 21.8.
+// streams read it from L2, which costs less than a launch of its own and a join. Both ways were
+// measured at 775 sizes (20 numbers of streams, key and query heads, D 64 and 128, 200 and 1000
+// slots, 8 to 256 MB). With 8 rows, where prefix_kernel's tiles are nearly empty, they cross at 48 to
+// 96 MB (with 2 rows they hardly differ, with 6 either wins); to 128 rows at 8 to 96; above, where the
+// streams' query heads share what they read and prefix_kernel has twice the rows to start with, at 8
+// to 192, the more slots the sooner. 8 key heads, D = 128,
+// 200 slots, own and not: 8 streams, 1 head each, 64 MB 13.3 and 11.2 us, 24 MB 9.0 and 10.7; 64
+// streams, 4 heads each, 48 MB 16.3 and 18.8, 96 MB 21.6 and 21.2. The choice by these three limits
+// costs 4, 1 and 3 % over the faster way on average in the three ranges, 47 % (5 us) at worst.
 constexpr int64_t own_prefix_bytes(int64_t rows) {
     return (rows <= swa::kAttendQueries ? 128 : rows <= 128 ? 24 : 64) << 20;
 }
@@ -240,8 +242,8 @@ Plan plan(int64_t B, int64_t H, int64_t Hkv, int64_t S, int64_t P, int64_t D, bo
     const int64_t G = H / Hkv, Q = swa::kAttendQueries, units = B * Hkv;
     if (G <= Q) {
         const bool own = P > 0 && (B == 1 || units * P <= own_prefix_bytes(B * G) / (4 * D));
-        // The time of a call in the keys that a CTA takes meanwhile, by the measured rates of the
-        // listed sizes: rounds of resident CTAs (4 an SM for D = 128, 6 for 64; a round that is
+        // The time of a call in the keys that a CTA takes meanwhile, by rates measured at the sizes
+        // below and others between: rounds of resident CTAs (4 an SM for D = 128, 6 for 64; a round that is
         // not full still takes 0.55 of its time, as its CTAs share the bandwidth among fewer), each
         // its keys and 70 for its start and end, 40 for the barriers of a cluster. Of D = 128,
         // S = 1000, 192 heads: 30.3, 20.8, 27.8, 30.1 us for C = 1, 2, 4, 8; 384 heads: 38.5,

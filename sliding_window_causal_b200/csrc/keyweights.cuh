@@ -167,9 +167,10 @@ __global__ void __launch_bounds__(kKwSimtThreads, 3)
 //   warps 2 .. 9  two warpgroups: p = 2^(s c + nlse) and the row sums of every second stage
 // Bound: one exp a band pair on the special-function unit (16 a clock and SM), 2 x the time of
 // the product at D = 128. 32 heads of 16384 tokens, W 4096 (1.88 G exponentials): 0.58 to 0.62 ms
-// by the clock that the power cap leaves, 0.7 of that unit's rate; with 1, 2, 3 or 4 of
-// each 8 exponentials as a polynomial on the FMA pipe an earlier form took 588, 614, 665 and 681
-// us against 582, as the warps' issue slots run out first. Two CTAs share an SM, so that one's
+// by the clock that the power cap leaves: the unit is 0.70 busy, the issue slots 0.39, and
+// what is missing is warps with scores to work on (a buffer goes back to the product when all of its
+// 128 columns are read). With 1, 2, 3 or 4 of each 8 exponentials as a polynomial on the FMA pipe an
+// earlier form took 588, 614, 665 and 681 us against 582. Two CTAs share an SM, so that one's
 // start and end overlap the other's work. Few keys and many queries: a cluster of C CTAs splits
 // the slices of one key tile and adds its sums in rank order through distributed shared memory.
 constexpr int kKwThreads = 320;

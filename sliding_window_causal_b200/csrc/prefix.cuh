@@ -20,11 +20,13 @@
 //
 // Measured, D = 128: 128 streams of 32 heads, 4 to a key head, behind 65536 keys (PAIR, 137 GFLOP):
 // 0.152 ms (0.165 where few keys dominate the rows), 0.9 PFLOP/s of the formula, 1.36 of the products
-// issued. 64 streams of 32 heads (!PAIR): 67 us more for 24576 more keys, 6.0 TB/s.
+// issued; P handed over in 1 or 4 parts instead of 2 0.157 and 0.154. What bounds it is a lane's
+// chain product, softmax, product, of which two lanes hide only a part (tensor pipe 0.52 busy). 64
+// streams of 32 heads (!PAIR): 67 us more for 24576 more keys, 6.0 TB/s.
 //
 // P is carried as hi + lo bf16 parts (2^-16 of a weight), so that the output is rounded once, as in
 // the streams' kernels, and a stream's precision does not depend on how many rows share the prefix.
-// !PAIR has room for the second product; PAIR is bound by the products. Of one part only, there
+// !PAIR has room for the second product; in PAIR it lengthens the chain. Of one part only, there
 // 0.125 ms, a key that holds much of a row's weight is off by up to 2^-8 of itself: queries scaled
 // by 8 gave 0.019 on outputs below 4 (0.011 if divided by the sum of the rounded weights) where two
 // parts give 0.0078, the output's own rounding. Two parts only in the tiles of such keys: 0.133 ms
