@@ -215,3 +215,39 @@ def test_a_stream_does_not_depend_on_its_neighbours(D, P):
     b = swa.prefix_decode(q, kp, vp, kc, vc, pos, S)
     assert torch.equal(a[1::2], b[1::2]) and not torch.equal(a[::2], b[::2])
     swa.device_status()
+
+
+@pytest.mark.parametrize("P", [4000, 30011])
+def test_two_streams_at_once_and_replayed(P):
+    """More than 128 rows to a key head: calls on two streams with workspaces of their own, and the
+    same calls captured into two graphs that replay side by side, equal calls alone."""
+    B, Hkv, G, D, S = 40, 2, 4, 128, 200
+    g = gen(P + 7)
+    sets = [(rand(g, B, Hkv * G, D), rand(g, Hkv, P, D), rand(g, Hkv, P, D), rand(g, B, Hkv, S, D), rand(g, B, Hkv, S, D),
+             torch.randint(0, 2 * S, (B,), generator=g, device=DEV)) for _ in range(2)]
+    want = [swa.prefix_decode(*s, S) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(10):
+        for x in range(2):
+            with torch.cuda.stream(streams[x]):
+                outs[x].append(swa.prefix_decode(*sets[x], S))
+    torch.cuda.synchronize()
+    graphs, kept = [], []
+    for x in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=streams[x]):
+            kept.append([swa.prefix_decode(*sets[x], S) for _ in range(5)])
+        graphs.append(gr)
+    for _ in range(3):
+        for o in kept[0] + kept[1]:
+            o.zero_()
+        torch.cuda.synchronize()
+        for x in range(2):
+            with torch.cuda.stream(streams[x]):
+                graphs[x].replay()
+        torch.cuda.synchronize()
+        for x in range(2):
+            assert all(torch.equal(o, want[x]) for o in outs[x] + kept[x])
+    swa.device_status()
