@@ -27,9 +27,9 @@
 // P is carried as hi + lo bf16 parts (2^-16 of a weight), so that the output is rounded once, as in
 // the streams' kernels, and a stream's precision does not depend on how many rows share the prefix.
 // !PAIR has room for the second product; in PAIR it lengthens the chain. Of one part only, there
-// 0.125 ms, a key that holds much of a row's weight is off by up to 2^-8 of itself: queries scaled
-// by 8 gave 0.019 on outputs below 4 (0.011 if divided by the sum of the rounded weights) where two
-// parts give 0.0078, the output's own rounding. Two parts only in the tiles of such keys: 0.133 ms
+// 0.125 ms, a key that holds much of a row's weight is off by up to 2^-8 of itself: for queries
+// scaled by 8 a float64 model of the roundings gives 0.020 on outputs below 4 (0.011 if divided by
+// the sum of the rounded weights) where two parts give 0.0078, the output's own rounding. Two parts only in the tiles of such keys: 0.133 ms
 // for even rows, but 0.225 for those.
 #pragma once
 #include <cuda_bf16.h>
