@@ -29,8 +29,8 @@
 // !PAIR has room for the second product; in PAIR it lengthens the chain. Of one part only, there
 // 0.125 ms, a key that holds much of a row's weight is off by up to 2^-8 of itself: for queries
 // scaled by 8 a float64 model of the roundings gives 0.020 on outputs below 4 (0.011 if divided by
-// the sum of the rounded weights) where two parts give 0.0078, the output's own rounding. Two parts only in the tiles of such keys: 0.133 ms
-// for even rows, but 0.225 for those.
+// the sum of the rounded weights) where two parts give 0.0078, the output's own rounding. Two parts
+// only in the tiles of such keys: 0.133 ms for even rows, but 0.225 for those.
 #pragma once
 #include <cuda_bf16.h>
 #include <math.h>
